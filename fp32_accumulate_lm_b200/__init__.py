@@ -37,6 +37,9 @@ __all__ = [
     "nvfp4_quantize_workspace_bytes", "status_string", "device_status", "DTYPE_BF16", "DTYPE_F16",
     "version", "set_fault_injection", "set_nvfp4_conversion", "STATUS", "lmhead_stream_status",
     "stream_status", "check", "test_hooks", "load_test_library",
+    "REDUCTIONS", "IGNORE_NONE", "lmhead_cross_entropy_f32", "lmhead_cross_entropy_grad",
+    "cross_entropy_workspace_bytes", "cross_entropy_grad_workspace_bytes", "cross_entropy_f32",
+    "cross_entropy_grad",
 ]
 
 STATUS = {
@@ -47,6 +50,8 @@ LMHEAD_OK = 0
 LMHEAD_ERR_TIMEOUT = 6
 DTYPE_BF16 = 0  # lmhead_dtype
 DTYPE_F16 = 1
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}  # lmhead_reduction
+IGNORE_NONE = -(2 ** 63)  # LMHEAD_IGNORE_NONE
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "liblmhead.so")
@@ -94,6 +99,16 @@ def _bind(lib, test: bool):
     lib.lmhead_nvfp4_quantize.restype = i32
     lib.lmhead_nvfp4_quantize_noalloc.argtypes = [vp, i64, i64, vp, vp, vp, vp]
     lib.lmhead_nvfp4_quantize_noalloc.restype = i32
+    size = ctypes.c_size_t
+    for name in ("cross_entropy", "cross_entropy_grad"):
+        f = getattr(lib, f"lmhead_{name}_workspace_bytes")
+        f.argtypes, f.restype = [i64, i64, i64, i64], size
+    lib.lmhead_cross_entropy_f32.argtypes = [vp, i32, i64, i64, vp, i64, f32, vp, vp, i64, f32, i32,
+                                             vp, vp, vp, size, vp]
+    lib.lmhead_cross_entropy_f32.restype = i32
+    lib.lmhead_cross_entropy_grad.argtypes = [vp, i32, i64, i64, vp, i64, f32, vp, vp, i64, f32,
+                                              i32, vp, vp, vp, vp, vp, i32, vp, size, vp]
+    lib.lmhead_cross_entropy_grad.restype = i32
     lib.lmhead_status_string.argtypes = [i32]
     lib.lmhead_status_string.restype = ctypes.c_char_p
     lib.lmhead_device_status.argtypes = [i32]
@@ -269,6 +284,37 @@ def nvfp4_quantize(W, workspace=None, out=None, stream=None, check: bool = False
                                g.data_ptr(), workspace.data_ptr(), nbytes, _stream_handle(stream))
     _finish(st, "lmhead_nvfp4_quantize", check, stream)
     return packed, scales, g
+
+
+def cross_entropy_workspace_bytes(rows: int, H: int, V: int, ignore_index=-100) -> int:
+    return int(_active().lmhead_cross_entropy_workspace_bytes(rows, H, V, _ignore(ignore_index)))
+
+
+def cross_entropy_grad_workspace_bytes(rows: int, H: int, V: int, ignore_index=-100) -> int:
+    return int(_active().lmhead_cross_entropy_grad_workspace_bytes(rows, H, V,
+                                                                   _ignore(ignore_index)))
+
+
+def lmhead_cross_entropy_f32(hidden_ptr: int, dtype: int, rows: int, H: int, w_ptr: int, V: int,
+                             alpha: float, bias_ptr: int, targets_ptr: int, ignore_index: int,
+                             z_loss: float, reduction: int, loss_ptr: int, lse_ptr: int,
+                             workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> int:
+    return _active().lmhead_cross_entropy_f32(
+        hidden_ptr or None, dtype, rows, H, w_ptr or None, V, alpha, bias_ptr or None,
+        targets_ptr or None, ignore_index, z_loss, reduction, loss_ptr or None, lse_ptr or None,
+        workspace_ptr or None, workspace_bytes, stream)
+
+
+def lmhead_cross_entropy_grad(hidden_ptr: int, dtype: int, rows: int, H: int, w_ptr: int, V: int,
+                              alpha: float, bias_ptr: int, targets_ptr: int, ignore_index: int,
+                              z_loss: float, reduction: int, lse_ptr: int, grad_loss_ptr: int,
+                              d_hidden_ptr: int, d_w_ptr: int, d_bias_ptr: int, accumulate: int,
+                              workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> int:
+    return _active().lmhead_cross_entropy_grad(
+        hidden_ptr or None, dtype, rows, H, w_ptr or None, V, alpha, bias_ptr or None,
+        targets_ptr or None, ignore_index, z_loss, reduction, lse_ptr or None,
+        grad_loss_ptr or None, d_hidden_ptr or None, d_w_ptr or None, d_bias_ptr or None,
+        accumulate, workspace_ptr or None, workspace_bytes, stream)
 
 
 def status_string(status: int) -> str:
@@ -684,3 +730,146 @@ def logits_w4a16_nvfp4(hidden, w_packed, w_scales, w_global_scale: float, alpha:
                                    out.data_ptr(), _stream_handle(stream))
     _finish(st, "lmhead_logits_w4a16_nvfp4", check, stream)
     return out
+
+
+# ---------------------------------------------------------------- training
+
+def _ignore(ignore_index) -> int:
+    return IGNORE_NONE if ignore_index is None else int(ignore_index)
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device and the call's stream as torch's current ones: the kernels launch on
+    this device, and memory allocated for the call belongs to the stream that uses it."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+            torch.cuda.default_stream(device)
+    _check(stream is None or stream.device == device, f"the stream must be one of {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _workspace(workspace, need: int, device):
+    import torch
+    if workspace is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+    _check(workspace.is_cuda and workspace.is_contiguous() and workspace.device == device,
+           "workspace must be a contiguous CUDA tensor on the inputs' device")
+    return workspace
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _check_head(hidden, W, targets, bias):
+    """The inputs of the cross entropy; returns (dtype code, rows, H, V)."""
+    import torch
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(hidden.dtype)
+    _check(dt is not None and W.dtype == hidden.dtype, "bf16 or fp16 operands of one dtype required")
+    _check(hidden.dim() == 2 and W.dim() == 2 and hidden.shape[1] == W.shape[1], "shape mismatch")
+    _check(hidden.is_cuda and W.is_cuda and hidden.is_contiguous() and W.is_contiguous(),
+           "contiguous CUDA tensors required")
+    rows, H = hidden.shape
+    V = W.shape[0]
+    _check(W.device == hidden.device, "hidden and W must be on one device")
+    _check(targets.dtype == torch.int32 and targets.is_cuda and targets.is_contiguous()
+           and tuple(targets.shape) == (rows,), "targets must be a contiguous int32 [rows] tensor")
+    _check(targets.device == hidden.device, "targets must be on the inputs' device")
+    if bias is not None:
+        _check(bias.dtype == hidden.dtype and bias.is_cuda and bias.is_contiguous()
+               and tuple(bias.shape) == (V,), "bias must be a contiguous [V] tensor of the dtype")
+        _check(bias.device == hidden.device, "bias must be on the inputs' device")
+    return dt, rows, H, V
+
+
+def _reduction(reduction: str) -> int:
+    _check(reduction in REDUCTIONS, f"reduction must be one of {sorted(REDUCTIONS)}")
+    return REDUCTIONS[reduction]
+
+
+def cross_entropy_f32(hidden, W, targets, alpha: float = 1.0, bias=None, ignore_index=-100,
+                      z_loss: float = 0.0, reduction: str = "mean", workspace=None, out=None,
+                      stream=None, check: bool = False):
+    """(loss, lse): the softmax cross entropy of the fp32 logits alpha * (hidden @ W^T + bias) against
+    each row's target (int32 CUDA tensor [rows]), without keeping the logits. A row's loss is
+    lse - z[target] + z_loss * lse^2; ``loss`` is fp32, the rows ("none"), or their sum or their
+    mean over the rows whose target is not ``ignore_index`` (0-dim); ``lse`` is fp32 [rows], for
+    cross_entropy_grad. Ignored rows have loss and lse 0 and may hold anything, NaN included;
+    ``ignore_index=None`` says that there are none, which saves a copy of the hidden rows. The
+    workspace (cross_entropy_workspace_bytes(rows, H, V, ignore_index) bytes) and the outputs
+    (``out`` = (loss, lse)) are allocated here, on the call's stream, unless given."""
+    import torch
+    dt, rows, H, V = _check_head(hidden, W, targets, bias)
+    red = _reduction(reduction)
+    dev = hidden.device
+    shape = (rows,) if reduction == "none" else ()
+    if out is not None:
+        _check_out(out[0], torch.float32, shape, dev, "out[0] (loss)")
+        _check_out(out[1], torch.float32, (rows,), dev, "out[1] (lse)")
+    with _on(dev, stream) as s:
+        loss, lse = out if out is not None else (
+            torch.empty(shape, dtype=torch.float32, device=dev),
+            torch.empty((rows,), dtype=torch.float32, device=dev))
+        ws = _workspace(workspace, cross_entropy_workspace_bytes(rows, H, V, ignore_index), dev)
+        st = lmhead_cross_entropy_f32(hidden.data_ptr(), dt, rows, H, W.data_ptr(), V, float(alpha),
+                                      _ptr(bias), targets.data_ptr(), _ignore(ignore_index),
+                                      float(z_loss), red, loss.data_ptr(), lse.data_ptr(),
+                                      ws.data_ptr(), _nbytes(ws), s.cuda_stream)
+        _finish(st, "lmhead_cross_entropy_f32", check, s)
+    return loss, lse
+
+
+def cross_entropy_grad(hidden, W, targets, lse, grad_loss, alpha: float = 1.0, bias=None,
+                       ignore_index=-100, z_loss: float = 0.0, reduction: str = "mean",
+                       accumulate: bool = False, workspace=None, out=None, stream=None,
+                       check: bool = False):
+    """(d_hidden, d_W, d_bias) of cross_entropy_f32's loss, in the operands' dtype, for the upstream
+    gradient ``grad_loss`` (fp32 CUDA tensor: [rows] for "none", else one element) and the forward
+    call's ``lse``; the other arguments are the forward call's. d_bias is None without a bias.
+    ``out`` = (d_hidden, d_W, d_bias) supplies the buffers; one given as None there is not computed.
+    ``accumulate`` adds d_W and d_bias to what their buffers hold (they must then be given): for
+    gradient accumulation, and for a table tied to the embedding. The workspace
+    (cross_entropy_grad_workspace_bytes(rows, H, V, ignore_index) bytes) is allocated here, on the
+    call's stream, unless given."""
+    import torch
+    dt, rows, H, V = _check_head(hidden, W, targets, bias)
+    red = _reduction(reduction)
+    dev = hidden.device
+    _check(lse.dtype == torch.float32 and lse.is_cuda and lse.is_contiguous()
+           and tuple(lse.shape) == (rows,) and lse.device == dev,
+           "lse must be the forward call's contiguous fp32 [rows] tensor")
+    _check(grad_loss.dtype == torch.float32 and grad_loss.is_cuda and grad_loss.is_contiguous()
+           and grad_loss.device == dev
+           and (tuple(grad_loss.shape) == (rows,) if reduction == "none" else grad_loss.numel() == 1),
+           "grad_loss must be a contiguous fp32 tensor of the loss's shape on the inputs' device")
+    _check(not accumulate or out is not None, "accumulate needs the buffers (out)")
+    if out is not None:
+        _check(len(out) == 3 and any(o is not None for o in out),
+               "out is (d_hidden, d_W, d_bias), one of them at least")
+        for o, what, shape in zip(out, ("d_hidden", "d_W", "d_bias"), ((rows, H), (V, H), (V,))):
+            if o is not None:
+                _check_out(o, hidden.dtype, shape, dev, what)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = (torch.empty_like(hidden), torch.empty_like(W),
+                   None if bias is None else torch.empty_like(bias))
+        ws = _workspace(workspace, cross_entropy_grad_workspace_bytes(rows, H, V, ignore_index), dev)
+        st = lmhead_cross_entropy_grad(hidden.data_ptr(), dt, rows, H, W.data_ptr(), V,
+                                       float(alpha), _ptr(bias), targets.data_ptr(),
+                                       _ignore(ignore_index), float(z_loss), red, lse.data_ptr(),
+                                       grad_loss.data_ptr(), _ptr(out[0]), _ptr(out[1]),
+                                       _ptr(out[2]), 1 if accumulate else 0, ws.data_ptr(),
+                                       _nbytes(ws), s.cuda_stream)
+        _finish(st, "lmhead_cross_entropy_grad", check, s)
+    return tuple(out)

@@ -23,6 +23,7 @@
 #include "lmhead_bf16.cuh"
 #include "lmhead_nvfp4.cuh"
 #include "lmhead_quant.cuh"
+#include "lmhead_xent.cuh"
 
 #ifndef LMHEAD_TEST_HOOKS
 #define LMHEAD_TEST_HOOKS 0
@@ -182,6 +183,10 @@ int current_device(DeviceInfo* out) {
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<4, false>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<1, true>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<2, true>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<false, false>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<false, true>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<true, false>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<true, true>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_w4a16_nvfp4_kernel<true>, d.smem_optin,
                           &d.nvfp4_static_smem[1]) ||
         !raise_smem_limit(lmh::lmhead_w4a16_nvfp4_kernel<false>, d.smem_optin,
@@ -928,3 +933,5 @@ int lmhead_logits_w4a16_nvfp4(const void* hidden, int64_t rows, int64_t H, const
 }
 
 }  // extern "C"
+
+#include "lmhead_train_entry.cuh"

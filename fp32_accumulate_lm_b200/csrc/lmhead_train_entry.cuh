@@ -1,0 +1,476 @@
+// Host side of the training entry points (declared in include/lmhead.h): argument checks, the
+// division of the work, the workspaces and the launches. Included at the end of lmhead.cu, whose
+// helpers (device set-up, tensor maps, launches) it uses.
+#pragma once
+
+namespace {
+
+constexpr int64_t kTrainMax = (int64_t)1 << 30;  // sizes below this leave room for rounding up
+
+int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+
+// Hands out 256-byte aligned parts of a workspace; with a null base it only counts.
+struct Carver {
+  uint8_t* base;
+  int64_t used = 0;
+  explicit Carver(void* b) : base(reinterpret_cast<uint8_t*>(b)) {}
+  template <typename T>
+  T* take(int64_t count) {
+    T* p = base != nullptr ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += round_up(count * (int64_t)sizeof(T), 256);
+    return p;
+  }
+};
+
+struct Region {
+  const void* p;
+  int64_t bytes;
+};
+
+// LMHEAD_ERR_ALIAS if an output overlaps another output or an input (null regions are skipped).
+int check_overlap(const Region* in, int n_in, const Region* out, int n_out) {
+  for (int i = 0; i < n_out; ++i) {
+    if (out[i].p == nullptr || out[i].bytes == 0) continue;
+    for (int j = 0; j < n_in; ++j)
+      if (in[j].p != nullptr && in[j].bytes > 0 &&
+          overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+        return LMHEAD_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p != nullptr && out[j].bytes > 0 &&
+          overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return LMHEAD_ERR_ALIAS;
+  }
+  return LMHEAD_OK;
+}
+
+// ---------------------------------------------------------------- cross entropy
+
+// The rows that count, side by side (only where a target can be ignored).
+struct XentPack {
+  uint4* hidden = nullptr;
+  int32_t *targets = nullptr, *place = nullptr, *row_of = nullptr, *n_rows = nullptr;
+};
+
+XentPack carve_pack(Carver& c, int64_t rows, int64_t H, bool ignoring) {
+  XentPack k;
+  if (!ignoring) return k;
+  k.hidden = c.take<uint4>(round_up(rows, lmh::kBK) * (H / 8));
+  k.targets = c.take<int32_t>(rows);
+  k.place = c.take<int32_t>(rows);
+  k.row_of = c.take<int32_t>(rows);
+  k.n_rows = c.take<int32_t>(1);
+  return k;
+}
+
+struct XentForward {
+  XentPack pack;
+  float2* partials;
+  float *target_z, *row_loss;
+};
+
+int64_t xent_chunks(int64_t V) { return (V + lmh::kXChunk - 1) / lmh::kXChunk; }
+
+XentForward carve_forward(Carver& c, int64_t rows, int64_t H, int64_t V, bool ignoring) {
+  XentForward f;
+  f.pack = carve_pack(c, rows, H, ignoring);
+  f.partials = c.take<float2>(xent_chunks(V) * rows);
+  f.target_z = c.take<float>(rows);
+  f.row_loss = c.take<float>(rows);
+  return f;
+}
+
+// The vocabulary in pieces of `piece` entries (a multiple of the tile width): d of a piece, 16 bits
+// a row and entry, takes about 128 MB, near what L2 holds, but a piece has at least 4096 entries,
+// so that its products fill the device at any number of rows. Pieces of equal length.
+// The splits of dH's K (a piece) make that product's tiles at least as many as the device has
+// units, at 512 entries a split or more; each split has an fp32 buffer of its own, and they are
+// added in order at the end.
+struct XentPieces {
+  int64_t rows_pad, piece;
+  int32_t n_pieces, splits;
+};
+
+XentPieces xent_pieces(int64_t rows, int64_t H, int64_t V) {
+  XentPieces x;
+  x.rows_pad = round_up(rows, 256);
+  const int64_t v_pad = round_up(V, lmh::kXN);
+  int64_t most = ((int64_t)128 << 20) / (2 * x.rows_pad) / lmh::kXN * lmh::kXN;
+  if (most < 4096) most = 4096;
+  x.n_pieces = (int32_t)((v_pad + most - 1) / most);
+  x.piece = round_up((v_pad + x.n_pieces - 1) / x.n_pieces, lmh::kXN);
+  x.n_pieces = (int32_t)((V + x.piece - 1) / x.piece);
+  const bool pair = rows > 128;
+  const int64_t units = pair ? 74 : 148;
+  const int64_t tiles =
+      (pair ? x.rows_pad / 256 : 1) * ((H + lmh::kXN - 1) / lmh::kXN);
+  int64_t s = (units + tiles - 1) / tiles;
+  const int64_t by_k = x.piece / 512;
+  if (s > by_k) s = by_k;
+  if (s > 32) s = 32;
+  x.splits = (int32_t)(s < 1 ? 1 : s);
+  return x;
+}
+
+struct XentBackward {
+  XentPack pack;
+  float4* row_info;
+  float* scale;
+  uint16_t* d[2];
+  float* dh_partial;
+};
+
+XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_t H,
+                            bool ignoring) {
+  XentBackward b;
+  b.pack = carve_pack(c, rows, H, ignoring);
+  b.row_info = c.take<float4>(rows);
+  b.scale = c.take<float>(2);
+  b.d[0] = c.take<uint16_t>(x.rows_pad * x.piece);
+  b.d[1] = x.n_pieces > 1 ? c.take<uint16_t>(x.rows_pad * x.piece) : b.d[0];
+  b.dh_partial = c.take<float>((int64_t)x.splits * x.rows_pad * H);
+  return b;
+}
+
+int check_xent_args(const void* hidden, int dtype, int64_t rows, int64_t H, const void* W,
+                    int64_t V, const void* bias, int64_t ignore_index, int reduction) {
+  const int st = check_f32_head_args(hidden, dtype, rows, H, W, V, bias);
+  if (st != LMHEAD_OK) return st;
+  if (rows >= kTrainMax || H >= kTrainMax || V >= kTrainMax) return LMHEAD_ERR_SHAPE;
+  if (ignore_index != LMHEAD_IGNORE_NONE &&
+      (ignore_index < INT32_MIN || ignore_index > INT32_MAX))
+    return LMHEAD_ERR_SHAPE;
+  if (reduction != LMHEAD_REDUCE_NONE && reduction != LMHEAD_REDUCE_SUM &&
+      reduction != LMHEAD_REDUCE_MEAN)
+    return LMHEAD_ERR_SHAPE;
+  return LMHEAD_OK;
+}
+
+int launch_pack(const XentPack& k, const void* hidden, const int32_t* targets, int64_t rows,
+                int64_t H, int64_t ignore_index, lmhead_stream_t stream) {
+  const unsigned blocks = (unsigned)((rows + lmh::kPackRows - 1) / lmh::kPackRows);
+  return launch_head(lmh::xent_pack_kernel, blocks, lmh::kPackThreads, 0, stream, 1u,
+                     reinterpret_cast<const uint4*>(hidden), targets, (int32_t)rows,
+                     (int32_t)(H / 8), (int32_t)ignore_index, k.hidden, k.targets, k.place,
+                     k.row_of, k.n_rows);
+}
+
+// A matrix of 16-bit elements in boxes of 64 columns by `box_rows` rows.
+int encode_xent(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                uint32_t box_rows) {
+  return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, cols * 2, rows, 128, box_rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+int launch_xent_gemm(const DeviceInfo& dev, bool fp16, bool pair, const lmh::XentMaps& maps,
+                     lmh::XentParams p, lmhead_stream_t stream) {
+  int64_t tiles = 0;
+  for (int i = 0; i < p.n_problems; ++i) {
+    const lmh::XentProblem& q = p.prob[i];
+    const int64_t m = q.m_rows ? p.rows : q.m_len;
+    const int64_t tm = pair ? 256 : 128;
+    tiles += ((m + tm - 1) / tm) * ((q.n_len + lmh::kXN - 1) / lmh::kXN) * q.splits;
+  }
+  if ((tiles << 1) > kInt32Max) return LMHEAD_ERR_SHAPE;
+  const size_t smem = pair ? lmh::XentTile<true>::kSmem : lmh::XentTile<false>::kSmem;
+  if ((int64_t)smem > dev.smem_optin) return LMHEAD_ERR_SHAPE;
+  auto kernel = pair ? (fp16 ? lmh::xent_gemm_kernel<true, true> : lmh::xent_gemm_kernel<true, false>)
+                     : (fp16 ? lmh::xent_gemm_kernel<false, true>
+                             : lmh::xent_gemm_kernel<false, false>);
+  return launch_head(kernel, (unsigned)(tiles << (pair ? 1 : 0)), lmh::kXThreads, smem, stream,
+                     pair ? 2u : 1u, maps, p);
+}
+
+// CTA pairs for more than 128 rows. With at most 128 rows, half of a pair's 256-row tile would be
+// empty and the call is bound by reading W; lone CTAs of 128 rows spend half the tensor time.
+bool xent_pairs(const DeviceInfo& dev, int64_t rows) {
+  return rows > 128 && dev.pair_clusters > 0 && !g_no_cta_pairs.load(std::memory_order_relaxed);
+}
+
+lmh::XentProblem xent_problem(int kind, int a_map, int b_map, int64_t n_len, int64_t k_len) {
+  lmh::XentProblem q = {};
+  q.kind = kind;
+  q.a_map = a_map;
+  q.b_map = b_map;
+  q.n_len = (int32_t)n_len;
+  q.k_len = (int32_t)k_len;
+  q.splits = 1;
+  return q;
+}
+
+int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, const void* W,
+                     int64_t V, float alpha, const void* bias, const int32_t* targets,
+                     int64_t ignore_index, float z_loss, int reduction, float* loss, float* lse,
+                     const XentForward& f, lmhead_stream_t stream) {
+  DeviceInfo dev;
+  int st = current_device(&dev);
+  if (st != LMHEAD_OK) return st;
+  const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
+  const XentPack& k = f.pack;
+  if (ignoring) {
+    st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
+    if (st != LMHEAD_OK) return st;
+  }
+  lmh::XentMaps maps = {};
+  st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
+                   ignoring ? round_up(rows, lmh::kBK) : rows, 64);
+  if (st != LMHEAD_OK) return st;
+  st = encode_xent(&maps.m[lmh::kMapW], W, H, V, 64);
+  if (st != LMHEAD_OK) return st;
+
+  lmh::XentParams p = {};
+  p.n_problems = 1;
+  p.prob[0] = xent_problem(lmh::kXentStats, lmh::kMapHidden, lmh::kMapW, V, H);
+  p.prob[0].m_rows = 1;
+  p.rows = (int32_t)rows;
+  p.n_rows = k.n_rows;
+  p.H = (int32_t)H;
+  p.group = 8;
+  p.alpha = alpha;
+  p.bias = reinterpret_cast<const uint16_t*>(bias);
+  p.targets = ignoring ? k.targets : targets;
+  p.partials = f.partials;
+  p.target_z = f.target_z;
+  p.wait = wait_cfg();
+  st = launch_xent_gemm(dev, dtype == LMHEAD_DTYPE_F16, xent_pairs(dev, rows), maps, p, stream);
+  if (st != LMHEAD_OK) return st;
+
+  float* row_loss = reduction == LMHEAD_REDUCE_NONE ? loss : f.row_loss;
+  st = launch_head(lmh::xent_fold_kernel,
+                   (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows), 1024, 0, stream, 1u,
+                   (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
+                   (int32_t)rows, (int32_t)V, (const int32_t*)k.place, p.targets,
+                   (const float*)f.target_z, z_loss, row_loss, lse);
+  if (st != LMHEAD_OK || reduction == LMHEAD_REDUCE_NONE) return st;
+  return launch_head(lmh::xent_reduce_kernel, 1, 1024, 0, stream, 1u, (const float*)row_loss,
+                     (int32_t)rows, (const int32_t*)k.n_rows,
+                     (int32_t)(reduction == LMHEAD_REDUCE_MEAN), loss);
+}
+
+int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, const void* W,
+                      int64_t V, float alpha, const void* bias, const int32_t* targets,
+                      int64_t ignore_index, float z_loss, int reduction, const float* lse,
+                      const float* grad_loss, void* d_hidden, void* d_W, void* d_bias,
+                      int accumulate, const XentPieces& x, const XentBackward& b,
+                      lmhead_stream_t stream) {
+  DeviceInfo dev;
+  int st = current_device(&dev);
+  if (st != LMHEAD_OK) return st;
+  const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
+  const bool fp16 = dtype == LMHEAD_DTYPE_F16;
+  const bool pair = xent_pairs(dev, rows);
+  const XentPack& k = b.pack;
+  if (ignoring) {
+    st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
+    if (st != LMHEAD_OK) return st;
+  }
+  const int32_t* tgt = ignoring ? k.targets : targets;
+  st = launch_head(lmh::xent_rows_kernel, 1, 1024, 0, stream, 1u, lse, tgt,
+                   (const int32_t*)k.row_of, (int32_t)rows, (const int32_t*)k.n_rows, (int32_t)V,
+                   grad_loss, (int32_t)(reduction == LMHEAD_REDUCE_NONE),
+                   (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.scale);
+  if (st != LMHEAD_OK) return st;
+
+  lmh::XentMaps maps = {};
+  st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
+                   ignoring ? round_up(rows, lmh::kBK) : rows, 64);
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, 64);
+  for (int i = 0; i < 2 && st == LMHEAD_OK; ++i) {
+    st = encode_xent(&maps.m[lmh::kMapD0 + i], b.d[i], x.piece, x.rows_pad, 64);
+    if (st == LMHEAD_OK)
+      st = encode_xent(&maps.m[lmh::kMapD0Store + i], b.d[i], x.piece, x.rows_pad, 32);
+  }
+  if (st == LMHEAD_OK && d_W != nullptr) st = encode_xent(&maps.m[lmh::kMapDw], d_W, H, V, 32);
+  if (st != LMHEAD_OK) return st;
+
+  lmh::XentParams p = {};
+  p.rows = (int32_t)rows;
+  p.n_rows = k.n_rows;
+  p.H = (int32_t)H;
+  p.rows_pad = (int32_t)x.rows_pad;
+  p.group = 8;
+  p.alpha = alpha;
+  p.bias = reinterpret_cast<const uint16_t*>(bias);
+  p.targets = tgt;
+  p.row_info = b.row_info;
+  p.scale = b.scale;
+  p.d_weight = reinterpret_cast<uint16_t*>(d_W);
+  p.dh_partial = b.dh_partial;
+  p.wait = wait_cfg();
+
+  auto start = [&](int c) { return (int64_t)c * x.piece; };
+  auto length = [&](int c) { return V - start(c) < x.piece ? V - start(c) : x.piece; };
+  auto logits_of = [&](int c) {
+    lmh::XentProblem q =
+        xent_problem(lmh::kXentDlogits, lmh::kMapHidden, lmh::kMapW, length(c), H);
+    q.m_rows = 1;
+    q.b_off = (int32_t)start(c);
+    q.out_map = lmh::kMapD0Store + (c & 1);
+    return q;
+  };
+  p.n_problems = 1;
+  p.prob[0] = logits_of(0);
+  st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
+  for (int c = 0; c < x.n_pieces && st == LMHEAD_OK; ++c) {
+    const int d_map = lmh::kMapD0 + (c & 1);
+    if (d_bias != nullptr) {
+      const unsigned blocks = (unsigned)((length(c) + lmh::kBiasCols - 1) / lmh::kBiasCols);
+      st = launch_head(fp16 ? lmh::xent_bias_kernel<true> : lmh::xent_bias_kernel<false>, blocks,
+                       256, 0, stream, 1u, (const uint16_t*)b.d[c & 1], (int32_t)x.piece,
+                       (int32_t)length(c), (int32_t)rows, (const int32_t*)k.n_rows,
+                       (const float*)b.scale, (int32_t)(accumulate != 0),
+                       reinterpret_cast<uint16_t*>(d_bias) + start(c));
+      if (st != LMHEAD_OK) return st;
+    }
+    p.n_problems = 0;
+    if (d_hidden != nullptr) {  // the longest tiles first
+      lmh::XentProblem q = xent_problem(lmh::kXentDhidden, d_map, lmh::kMapW, H, length(c));
+      q.m_rows = 1;
+      q.b_mn = 1;
+      q.b_off = (int32_t)start(c);
+      q.b_k = 1;
+      q.splits = x.splits;
+      q.add = c > 0;
+      p.prob[p.n_problems++] = q;
+    }
+    if (d_W != nullptr) {
+      lmh::XentProblem q = xent_problem(lmh::kXentDweight, d_map, lmh::kMapHidden, H, 0);
+      q.m_len = (int32_t)length(c);
+      q.k_rows = 1;
+      q.a_mn = q.b_mn = 1;
+      q.out_off = (int32_t)start(c);
+      q.out_map = lmh::kMapDw;
+      q.add = accumulate != 0;
+      p.prob[p.n_problems++] = q;
+    }
+    if (c + 1 < x.n_pieces) p.prob[p.n_problems++] = logits_of(c + 1);
+    if (p.n_problems > 0) st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
+  }
+  if (st != LMHEAD_OK || d_hidden == nullptr) return st;
+  const int64_t vecs = rows * (H / 8);
+  return launch_head(
+      fp16 ? lmh::xent_finish_hidden_kernel<true> : lmh::xent_finish_hidden_kernel<false>,
+      (unsigned)((vecs + lmh::kFinishThreads - 1) / lmh::kFinishThreads), lmh::kFinishThreads, 0,
+      stream, 1u, (const float*)b.dh_partial, x.splits, x.rows_pad * H, (int32_t)rows, (int32_t)H,
+      (const int32_t*)k.place, (const float*)b.scale, reinterpret_cast<uint4*>(d_hidden));
+}
+
+int cleared(int st) {
+  if (st != LMHEAD_OK) (void)cudaGetLastError();  // leave no stale error for the next call
+  return st;
+}
+
+// Zeros in `bytes` bytes of device memory, on the stream.
+int write_zeros(void* p, int64_t bytes, lmhead_stream_t stream) {
+  if (p == nullptr || bytes == 0) return LMHEAD_OK;
+  return cudaMemsetAsync(p, 0, (size_t)bytes, (cudaStream_t)stream) == cudaSuccess
+             ? LMHEAD_OK
+             : LMHEAD_ERR_LAUNCH;
+}
+
+bool xent_sizes_ok(int64_t rows, int64_t H, int64_t V) {
+  return rows > 0 && H > 0 && V > 0 && rows < kTrainMax && H < kTrainMax && V < kTrainMax;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lmhead_cross_entropy_workspace_bytes(int64_t rows, int64_t H, int64_t V,
+                                            int64_t ignore_index) {
+  if (!xent_sizes_ok(rows, H, V)) return 0;
+  Carver c(nullptr);
+  carve_forward(c, rows, H, V, ignore_index != LMHEAD_IGNORE_NONE);
+  return (size_t)c.used;
+}
+
+size_t lmhead_cross_entropy_grad_workspace_bytes(int64_t rows, int64_t H, int64_t V,
+                                                 int64_t ignore_index) {
+  if (!xent_sizes_ok(rows, H, V)) return 0;
+  Carver c(nullptr);
+  carve_backward(c, xent_pieces(rows, H, V), rows, H, ignore_index != LMHEAD_IGNORE_NONE);
+  return (size_t)c.used;
+}
+
+int lmhead_cross_entropy_f32(const void* hidden, int dtype, int64_t rows, int64_t H,
+                             const void* W, int64_t V, float alpha, const void* bias,
+                             const int32_t* targets, int64_t ignore_index, float z_loss,
+                             int reduction, float* loss, float* lse, void* workspace,
+                             size_t workspace_bytes, lmhead_stream_t stream) {
+  int st = check_xent_args(hidden, dtype, rows, H, W, V, bias, ignore_index, reduction);
+  if (st != LMHEAD_OK) return st;
+  if (rows == 0) {
+    if (reduction == LMHEAD_REDUCE_NONE) return LMHEAD_OK;
+    if (loss == nullptr) return LMHEAD_ERR_NULL;
+    if (!aligned(loss, 4)) return LMHEAD_ERR_ALIGN;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    return st != LMHEAD_OK ? st : cleared(write_zeros(loss, 4, stream));
+  }
+  if (targets == nullptr || loss == nullptr || lse == nullptr || workspace == nullptr)
+    return LMHEAD_ERR_NULL;
+  if (!aligned(targets, 4) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return LMHEAD_ERR_ALIGN;
+  if (workspace_bytes < lmhead_cross_entropy_workspace_bytes(rows, H, V, ignore_index))
+    return LMHEAD_ERR_SHAPE;
+  const Region in[4] = {
+      {hidden, rows * H * 2}, {W, V * H * 2}, {bias, V * 2}, {targets, rows * 4}};
+  const Region out[3] = {{loss, reduction == LMHEAD_REDUCE_NONE ? rows * 4 : 4},
+                         {lse, rows * 4},
+                         {workspace, (int64_t)workspace_bytes}};
+  st = check_overlap(in, 4, out, 3);
+  if (st != LMHEAD_OK) return st;
+  Carver c(workspace);
+  const XentForward f = carve_forward(c, rows, H, V, ignore_index != LMHEAD_IGNORE_NONE);
+  return cleared(run_xent_forward(hidden, dtype, rows, H, W, V, alpha, bias, targets, ignore_index,
+                                  z_loss, reduction, loss, lse, f, stream));
+}
+
+int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64_t H,
+                              const void* W, int64_t V, float alpha, const void* bias,
+                              const int32_t* targets, int64_t ignore_index, float z_loss,
+                              int reduction, const float* lse, const float* grad_loss,
+                              void* d_hidden, void* d_W, void* d_bias, int accumulate,
+                              void* workspace, size_t workspace_bytes, lmhead_stream_t stream) {
+  int st = check_xent_args(hidden, dtype, rows, H, W, V, bias, ignore_index, reduction);
+  if (st != LMHEAD_OK) return st;
+  if (d_hidden == nullptr && d_W == nullptr && d_bias == nullptr && rows > 0)
+    return LMHEAD_ERR_NULL;
+  if ((d_hidden != nullptr && !aligned(d_hidden, 16)) || (d_W != nullptr && !aligned(d_W, 16)) ||
+      (d_bias != nullptr && !aligned(d_bias, 2)))
+    return LMHEAD_ERR_ALIGN;
+  if (rows == 0) {
+    if (accumulate) return LMHEAD_OK;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st == LMHEAD_OK) st = write_zeros(d_W, V * H * 2, stream);
+    if (st == LMHEAD_OK) st = write_zeros(d_bias, V * 2, stream);
+    return cleared(st);
+  }
+  if (targets == nullptr || lse == nullptr || grad_loss == nullptr || workspace == nullptr)
+    return LMHEAD_ERR_NULL;
+  if (!aligned(targets, 4) || !aligned(lse, 4) || !aligned(grad_loss, 4) ||
+      !aligned(workspace, 256))
+    return LMHEAD_ERR_ALIGN;
+  if (workspace_bytes < lmhead_cross_entropy_grad_workspace_bytes(rows, H, V, ignore_index))
+    return LMHEAD_ERR_SHAPE;
+  const Region in[6] = {{hidden, rows * H * 2},
+                        {W, V * H * 2},
+                        {bias, V * 2},
+                        {targets, rows * 4},
+                        {lse, rows * 4},
+                        {grad_loss, reduction == LMHEAD_REDUCE_NONE ? rows * 4 : 4}};
+  const Region out[4] = {{d_hidden, rows * H * 2},
+                         {d_W, V * H * 2},
+                         {d_bias, V * 2},
+                         {workspace, (int64_t)workspace_bytes}};
+  st = check_overlap(in, 6, out, 4);
+  if (st != LMHEAD_OK) return st;
+  const XentPieces x = xent_pieces(rows, H, V);
+  Carver c(workspace);
+  const XentBackward b = carve_backward(c, x, rows, H, ignore_index != LMHEAD_IGNORE_NONE);
+  return cleared(run_xent_backward(hidden, dtype, rows, H, W, V, alpha, bias, targets, ignore_index,
+                                   z_loss, reduction, lse, grad_loss, d_hidden, d_W, d_bias,
+                                   accumulate, x, b, stream));
+}
+
+}  // extern "C"

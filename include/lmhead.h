@@ -275,6 +275,70 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
                                   uint8_t* w_scales, float* w_global_scale,
                                   lmhead_stream_t stream);
 
+/*
+ * Softmax cross entropy over the vocabulary, in training, without keeping the logits. With z[r, v]
+ * the fp32 logits of lmhead_logits_f32 (alpha and the bias included) and t = targets[r],
+ *   lse[r]    = log sum_v exp(z[r, v])
+ *   row r     = lse[r] - z[r, t] + z_loss * lse[r]^2
+ *   loss      = the rows (LMHEAD_REDUCE_NONE, fp32 [rows]), or their sum or their mean over the
+ *               rows that count (LMHEAD_REDUCE_SUM, LMHEAD_REDUCE_MEAN; one fp32)
+ * A row whose target is `ignore_index` does not count: its loss and lse are 0, and nothing that its
+ * hidden row holds (NaN, infinities) reaches any output. With no row that counts the sum and the
+ * mean are 0. ignore_index = LMHEAD_IGNORE_NONE says that every row counts, which saves a copy of
+ * the hidden rows. Any other target outside [0, V) makes the row's loss NaN. z may be -inf (a bias
+ * of -inf takes an entry out of the vocabulary), as long as a row has one finite logit; a NaN or
+ * +inf logit makes the row's loss and lse NaN.
+ *
+ * lmhead_cross_entropy_grad gives the gradients for the upstream gradient `grad_loss` (fp32 [rows]
+ * for LMHEAD_REDUCE_NONE, else one fp32), recomputing the logits from hidden and W:
+ *   dz[r, v]  = g_r * ((1 + 2 * z_loss * lse[r]) * exp(z[r, v] - lse[r]) - [v == t])
+ *   d_hidden  = alpha * dz @ W                 dtype [rows, H] (0 for rows that do not count)
+ *   d_W       = alpha * dz^T @ hidden          dtype [V, H]
+ *   d_bias    = alpha * sum_r dz[r]            dtype [V]
+ * with g_r = grad_loss[r], grad_loss, or grad_loss / (rows that count). `lse` is the forward call's.
+ * accumulate != 0 adds d_W and d_bias to what these buffers hold (in fp32, rounded once); d_hidden
+ * is always written. Any of the three may be NULL and is then not computed, but not all of them. A
+ * row with a target outside [0, V) that is not ignored has NaN gradients, and so have d_W and
+ * d_bias then. The products take dz in the operands' 16-bit type (each entry off by at most half a
+ * step of that type, fp16 with a common power of two taken out); every sum is fp32.
+ *
+ * Both are deterministic. The loss of a row does not depend on the other rows of the call; the
+ * gradients' sums run over the rows that count in order.
+ *
+ *   hidden, W, bias, dtype, alpha: as lmhead_logits_f32; d_hidden, d_W 16-byte aligned, d_bias 2
+ *   targets    int32 [rows], 4-byte aligned
+ *   lse        fp32 [rows], 4-byte aligned (output of the first, input of the second)
+ *   loss       fp32 [rows] or [1], grad_loss likewise, 4-byte aligned
+ *   workspace  at least the *_workspace_bytes of the same sizes, 256-byte aligned
+ *   sizes      rows, H, V < 2^30
+ * rows == 0: the loss of REDUCE_SUM and REDUCE_MEAN is written as 0, and so are d_W and d_bias unless
+ * they accumulate. Outputs and the workspace must not overlap each other or the inputs. The first
+ * enqueues three to four kernels, the second four to five and one more for each piece of the
+ * vocabulary. Each returns an lmhead_status.
+ */
+#define LMHEAD_IGNORE_NONE INT64_MIN
+typedef enum {
+  LMHEAD_REDUCE_NONE = 0,
+  LMHEAD_REDUCE_SUM = 1,
+  LMHEAD_REDUCE_MEAN = 2
+} lmhead_reduction;
+
+size_t lmhead_cross_entropy_workspace_bytes(int64_t rows, int64_t H, int64_t V,
+                                            int64_t ignore_index);
+int lmhead_cross_entropy_f32(const void* hidden, int dtype, int64_t rows, int64_t H,
+                             const void* W, int64_t V, float alpha, const void* bias,
+                             const int32_t* targets, int64_t ignore_index, float z_loss,
+                             int reduction, float* loss, float* lse, void* workspace,
+                             size_t workspace_bytes, lmhead_stream_t stream);
+size_t lmhead_cross_entropy_grad_workspace_bytes(int64_t rows, int64_t H, int64_t V,
+                                                 int64_t ignore_index);
+int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64_t H,
+                              const void* W, int64_t V, float alpha, const void* bias,
+                              const int32_t* targets, int64_t ignore_index, float z_loss,
+                              int reduction, const float* lse, const float* grad_loss,
+                              void* d_hidden, void* d_W, void* d_bias, int accumulate,
+                              void* workspace, size_t workspace_bytes, lmhead_stream_t stream);
+
 /* A static English description of a status code. Never NULL. */
 const char* lmhead_status_string(int status);
 
