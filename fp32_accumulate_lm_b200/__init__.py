@@ -39,7 +39,8 @@ __all__ = [
     "stream_status", "check", "test_hooks", "load_test_library",
     "REDUCTIONS", "IGNORE_NONE", "lmhead_cross_entropy_f32", "lmhead_cross_entropy_grad",
     "cross_entropy_workspace_bytes", "cross_entropy_grad_workspace_bytes", "cross_entropy_f32",
-    "cross_entropy_grad",
+    "cross_entropy_grad", "lmhead_embedding", "lmhead_embedding_grad",
+    "embedding_grad_workspace_bytes", "embedding", "embedding_grad",
 ]
 
 STATUS = {
@@ -109,6 +110,13 @@ def _bind(lib, test: bool):
     lib.lmhead_cross_entropy_grad.argtypes = [vp, i32, i64, i64, vp, i64, f32, vp, vp, i64, f32,
                                               i32, vp, vp, vp, vp, vp, i32, vp, size, vp]
     lib.lmhead_cross_entropy_grad.restype = i32
+    lib.lmhead_embedding.argtypes = [vp, i64, vp, i32, i64, i64, i64, f32, vp, vp]
+    lib.lmhead_embedding.restype = i32
+    lib.lmhead_embedding_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.lmhead_embedding_grad_workspace_bytes.restype = size
+    lib.lmhead_embedding_grad.argtypes = [vp, i32, vp, i64, i64, i64, i64, f32, vp, i32, vp, size,
+                                          vp]
+    lib.lmhead_embedding_grad.restype = i32
     lib.lmhead_status_string.argtypes = [i32]
     lib.lmhead_status_string.restype = ctypes.c_char_p
     lib.lmhead_device_status.argtypes = [i32]
@@ -315,6 +323,24 @@ def lmhead_cross_entropy_grad(hidden_ptr: int, dtype: int, rows: int, H: int, w_
         targets_ptr or None, ignore_index, z_loss, reduction, lse_ptr or None,
         grad_loss_ptr or None, d_hidden_ptr or None, d_w_ptr or None, d_bias_ptr or None,
         accumulate, workspace_ptr or None, workspace_bytes, stream)
+
+
+def lmhead_embedding(ids_ptr: int, tokens: int, w_ptr: int, dtype: int, V: int, v_begin: int,
+                     H: int, scale: float, out_ptr: int, stream: int = 0) -> int:
+    return _active().lmhead_embedding(ids_ptr or None, tokens, w_ptr or None, dtype, V, v_begin, H,
+                                      scale, out_ptr or None, stream)
+
+
+def embedding_grad_workspace_bytes(tokens: int, V: int, H: int) -> int:
+    return int(_active().lmhead_embedding_grad_workspace_bytes(tokens, V, H))
+
+
+def lmhead_embedding_grad(d_out_ptr: int, dtype: int, ids_ptr: int, tokens: int, V: int,
+                          v_begin: int, H: int, scale: float, d_w_ptr: int, accumulate: int,
+                          workspace_ptr: int, workspace_bytes: int, stream: int = 0) -> int:
+    return _active().lmhead_embedding_grad(d_out_ptr or None, dtype, ids_ptr or None, tokens, V,
+                                           v_begin, H, scale, d_w_ptr or None, accumulate,
+                                           workspace_ptr or None, workspace_bytes, stream)
 
 
 def status_string(status: int) -> str:
@@ -873,3 +899,70 @@ def cross_entropy_grad(hidden, W, targets, lse, grad_loss, alpha: float = 1.0, b
                                        _nbytes(ws), s.cuda_stream)
         _finish(st, "lmhead_cross_entropy_grad", check, s)
     return tuple(out)
+
+
+def _check_table(t, what: str):
+    import torch
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(t.dtype)
+    _check(dt is not None, f"{what} must be bf16 or fp16")
+    _check(t.is_cuda and t.is_contiguous(), f"{what} must be a contiguous CUDA tensor")
+    return dt
+
+
+def _check_ids(ids, device):
+    import torch
+    _check(ids.dtype == torch.int32 and ids.is_cuda and ids.is_contiguous(),
+           "ids must be a contiguous int32 CUDA tensor")
+    _check(ids.device == device, "ids must be on the table's device")
+
+
+def embedding(ids, W, scale: float = 1.0, v_begin: int = 0, out=None, stream=None,
+              check: bool = False):
+    """Rows of the bf16 or fp16 table W [V, H] at the int32 ids (any shape), times ``scale``:
+    [*ids.shape, H] in W's dtype. An id outside [v_begin, v_begin + V) gives a row of zeros, so
+    each GPU of a table split by vocabulary calls this with its slice and the results are summed."""
+    import torch
+    dt = _check_table(W, "W")
+    _check(W.dim() == 2, "W must be a matrix")
+    _check_ids(ids, W.device)
+    V, H = W.shape
+    shape = (*ids.shape, H)
+    if out is not None:
+        _check_out(out, W.dtype, shape, W.device, "out")
+    with _on(W.device, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=W.dtype, device=W.device)
+        st = lmhead_embedding(ids.data_ptr(), ids.numel(), W.data_ptr(), dt, V, int(v_begin), H,
+                              float(scale), out.data_ptr(), s.cuda_stream)
+        _finish(st, "lmhead_embedding", check, s)
+    return out
+
+
+def embedding_grad(d_out, ids, V: int, scale: float = 1.0, v_begin: int = 0,
+                   accumulate: bool = False, workspace=None, out=None, stream=None,
+                   check: bool = False):
+    """The gradient of ``embedding`` for its table of V rows: [V, H] in d_out's dtype, from d_out
+    [*ids.shape, H]. ``accumulate`` adds to what ``out`` holds (it must then be given) and touches
+    only the rows that occur: for gradient accumulation, and for a table tied to the head, after
+    cross_entropy_grad has written the head's part. The workspace
+    (embedding_grad_workspace_bytes(tokens, V, H) bytes) is allocated here, on the call's stream,
+    unless given."""
+    import torch
+    dt = _check_table(d_out, "d_out")
+    dev = d_out.device
+    _check_ids(ids, dev)
+    _check(d_out.dim() >= 1 and tuple(d_out.shape[:-1]) == tuple(ids.shape),
+           "d_out must be [*ids.shape, H]")
+    H, tokens, V = d_out.shape[-1], ids.numel(), int(V)
+    _check(not accumulate or out is not None, "accumulate needs the buffer (out)")
+    if out is not None:
+        _check_out(out, d_out.dtype, (V, H), dev, "out")
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((V, H), dtype=d_out.dtype, device=dev)
+        ws = _workspace(workspace, embedding_grad_workspace_bytes(tokens, V, H), dev)
+        st = lmhead_embedding_grad(d_out.data_ptr(), dt, ids.data_ptr(), tokens, V, int(v_begin), H,
+                                   float(scale), out.data_ptr(), 1 if accumulate else 0,
+                                   ws.data_ptr(), _nbytes(ws), s.cuda_stream)
+        _finish(st, "lmhead_embedding_grad", check, s)
+    return out

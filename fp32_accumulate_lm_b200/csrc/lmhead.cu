@@ -24,6 +24,7 @@
 #include "lmhead_nvfp4.cuh"
 #include "lmhead_quant.cuh"
 #include "lmhead_xent.cuh"
+#include "lmhead_embed.cuh"
 
 #ifndef LMHEAD_TEST_HOOKS
 #define LMHEAD_TEST_HOOKS 0
@@ -231,10 +232,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // work still follows it. Returns an lmhead_status.
 // `cluster` = 2 launches the grid as CTA pairs (clusters of two along x).
 template <typename... KArgs, typename... Args>
-int launch_head(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
+int launch_head(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem,
                 lmhead_stream_t stream, unsigned cluster, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;

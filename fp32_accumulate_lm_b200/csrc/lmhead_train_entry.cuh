@@ -371,6 +371,105 @@ bool xent_sizes_ok(int64_t rows, int64_t H, int64_t V) {
   return rows > 0 && H > 0 && V > 0 && rows < kTrainMax && H < kTrainMax && V < kTrainMax;
 }
 
+// ---------------------------------------------------------------- embedding
+
+struct EmbedPlan {
+  int32_t passes, bits;  // of the sort
+  int32_t tile, tiles;   // sorted entries per block of the sums
+};
+
+// Digits of equal width, as few passes as 9 bits a digit allow, that hold every id and the mark V.
+// The sums' tile is 64 entries, and longer for many tokens, so that a run through all of them
+// is joined from at most 256 parts (or tiles of 1024); at 16384 tokens 64 entries still give 256
+// blocks a column slice.
+EmbedPlan embed_plan(int64_t tokens, int64_t V) {
+  EmbedPlan e;
+  int bits = 1;
+  while (((int64_t)1 << bits) <= V) ++bits;
+  e.passes = (bits + lmh::kSortBits - 1) / lmh::kSortBits;
+  e.bits = (bits + e.passes - 1) / e.passes;
+  e.tile = 64;
+  while (e.tile < lmh::kSumTileMax && (int64_t)e.tile * 256 < tokens) e.tile *= 2;
+  e.tiles = (int32_t)((tokens + e.tile - 1) / e.tile);
+  return e;
+}
+
+struct EmbedScratch {
+  int32_t *keys[2], *pos[2], *hist;
+  float* part;
+};
+
+EmbedScratch carve_embed(Carver& c, const EmbedPlan& e, int64_t tokens, int64_t H) {
+  EmbedScratch s;
+  for (int i = 0; i < 2; ++i) {
+    s.keys[i] = c.take<int32_t>(tokens);
+    s.pos[i] = c.take<int32_t>(tokens);
+  }
+  s.hist = c.take<int32_t>((int64_t)e.passes * lmh::kSortCtas * lmh::kSortDigits);
+  s.part = c.take<float>((int64_t)e.tiles * 2 * H);
+  return s;
+}
+
+// The sizes and the table's place in the vocabulary; token ids are int32.
+int check_embed_sizes(int dtype, int64_t tokens, int64_t V, int64_t v_begin, int64_t H) {
+  if (dtype != LMHEAD_DTYPE_BF16 && dtype != LMHEAD_DTYPE_F16) return LMHEAD_ERR_SHAPE;
+  if (tokens < 0 || V <= 0 || H <= 0) return LMHEAD_ERR_SHAPE;
+  if (H % 8 != 0) return LMHEAD_ERR_ALIGN;
+  if (tokens >= kTrainMax || V >= kTrainMax || H >= kTrainMax) return LMHEAD_ERR_SHAPE;
+  if (v_begin < 0 || v_begin > kInt32Max || V > (int64_t)kInt32Max + 1 - v_begin)
+    return LMHEAD_ERR_SHAPE;
+  return LMHEAD_OK;
+}
+
+int run_embed_grad(const DeviceInfo& dev, const void* d_out, int dtype, const int32_t* ids,
+                   int64_t tokens, int64_t V, int64_t v_begin, int64_t H, float scale, void* d_W,
+                   int accumulate, const EmbedPlan& e, const EmbedScratch& s,
+                   lmhead_stream_t stream) {
+  lmh::EmbedSortParams q = {};
+  q.ids = ids;
+  q.tokens = (int32_t)tokens;
+  q.v_begin = (int32_t)v_begin;
+  q.V = (int32_t)V;
+  q.passes = e.passes;
+  q.bits = e.bits;
+  for (int i = 0; i < 2; ++i) {
+    q.keys[i] = s.keys[i];
+    q.pos[i] = s.pos[i];
+  }
+  q.hist = s.hist;
+  unsigned clusters = 1;
+  if (!accumulate) {
+    q.zero = reinterpret_cast<uint4*>(d_W);
+    q.zero_vecs = V * (H / 8);
+    // two CTAs of 1024 threads an SM, or as many as the table has work for
+    int64_t fill = (q.zero_vecs + 4 * lmh::kSortThreads - 1) / (4 * lmh::kSortThreads);
+    if (fill > 2 * dev.num_sms) fill = 2 * dev.num_sms;
+    clusters += (unsigned)((fill + lmh::kSortCtas - 1) / lmh::kSortCtas);
+  }
+  int st = launch_head(lmh::embed_sort_kernel, clusters * lmh::kSortCtas, lmh::kSortThreads, 0,
+                       stream, lmh::kSortCtas, q);
+  if (st != LMHEAD_OK) return st;
+  const bool fp16 = dtype == LMHEAD_DTYPE_F16;
+  lmh::EmbedSumParams p = {};
+  p.keys = s.keys[(e.passes - 1) & 1];
+  p.pos = s.pos[(e.passes - 1) & 1];
+  p.tokens = (int32_t)tokens;
+  p.V = (int32_t)V;
+  p.H = (int32_t)H;
+  p.tile = e.tile;
+  p.d_out = reinterpret_cast<const uint16_t*>(d_out);
+  p.scale = scale;
+  p.add = accumulate != 0;
+  p.d_weight = reinterpret_cast<uint16_t*>(d_W);
+  p.part = s.part;
+  const unsigned slices = (unsigned)((H + lmh::kSumCols - 1) / lmh::kSumCols);
+  st = launch_head(fp16 ? lmh::embed_sum_kernel<true> : lmh::embed_sum_kernel<false>,
+                   dim3((unsigned)e.tiles, slices), lmh::kSumThreads, 0, stream, 1u, p);
+  if (st != LMHEAD_OK || e.tiles == 1) return st;
+  return launch_head(fp16 ? lmh::embed_join_kernel<true> : lmh::embed_join_kernel<false>,
+                     dim3((unsigned)(e.tiles - 1), slices), lmh::kSumThreads, 0, stream, 1u, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -471,6 +570,70 @@ int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64
   return cleared(run_xent_backward(hidden, dtype, rows, H, W, V, alpha, bias, targets, ignore_index,
                                    z_loss, reduction, lse, grad_loss, d_hidden, d_W, d_bias,
                                    accumulate, x, b, stream));
+}
+
+int lmhead_embedding(const int32_t* ids, int64_t tokens, const void* W, int dtype, int64_t V,
+                     int64_t v_begin, int64_t H, float scale, void* out, lmhead_stream_t stream) {
+  int st = check_embed_sizes(dtype, tokens, V, v_begin, H);
+  if (st != LMHEAD_OK || tokens == 0) return st;
+  if (ids == nullptr || W == nullptr || out == nullptr) return LMHEAD_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(W, 16) || !aligned(out, 16)) return LMHEAD_ERR_ALIGN;
+  const Region in[2] = {{ids, tokens * 4}, {W, V * H * 2}};
+  const Region o[1] = {{out, tokens * H * 2}};
+  st = check_overlap(in, 2, o, 1);
+  if (st != LMHEAD_OK) return st;
+  const int64_t pieces = (H / 8 + lmh::kEmbedVecs - 1) / lmh::kEmbedVecs;
+  const int64_t blocks =
+      (tokens * pieces + lmh::kEmbedThreads / 32 - 1) / (lmh::kEmbedThreads / 32);
+  if (blocks > kInt32Max) return LMHEAD_ERR_SHAPE;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != LMHEAD_OK) return st;
+  return cleared(launch_head(
+      dtype == LMHEAD_DTYPE_F16 ? lmh::embed_kernel<true> : lmh::embed_kernel<false>,
+      (unsigned)blocks, lmh::kEmbedThreads, 0, stream, 1u, ids, tokens, (int32_t)v_begin,
+      (int32_t)V, reinterpret_cast<const uint4*>(W), (int32_t)(H / 8), (int32_t)pieces, scale,
+      reinterpret_cast<uint4*>(out)));
+}
+
+size_t lmhead_embedding_grad_workspace_bytes(int64_t tokens, int64_t V, int64_t H) {
+  if (tokens <= 0 || V <= 0 || H <= 0 || tokens >= kTrainMax || V >= kTrainMax || H >= kTrainMax)
+    return 0;
+  Carver c(nullptr);
+  carve_embed(c, embed_plan(tokens, V), tokens, H);
+  return (size_t)c.used;
+}
+
+int lmhead_embedding_grad(const void* d_out, int dtype, const int32_t* ids, int64_t tokens,
+                          int64_t V, int64_t v_begin, int64_t H, float scale, void* d_W,
+                          int accumulate, void* workspace, size_t workspace_bytes,
+                          lmhead_stream_t stream) {
+  int st = check_embed_sizes(dtype, tokens, V, v_begin, H);
+  if (st != LMHEAD_OK) return st;
+  if (d_W == nullptr) return LMHEAD_ERR_NULL;
+  if (!aligned(d_W, 16)) return LMHEAD_ERR_ALIGN;
+  if (tokens == 0 && accumulate) return LMHEAD_OK;
+  DeviceInfo dev;
+  if (tokens == 0) {
+    st = current_device(&dev);
+    return st != LMHEAD_OK ? st : cleared(write_zeros(d_W, V * H * 2, stream));
+  }
+  if (d_out == nullptr || ids == nullptr || workspace == nullptr) return LMHEAD_ERR_NULL;
+  if (!aligned(d_out, 16) || !aligned(ids, 4) || !aligned(workspace, 256)) return LMHEAD_ERR_ALIGN;
+  if (workspace_bytes < lmhead_embedding_grad_workspace_bytes(tokens, V, H))
+    return LMHEAD_ERR_SHAPE;
+  const Region in[2] = {{d_out, tokens * H * 2}, {ids, tokens * 4}};
+  const Region out[2] = {{d_W, V * H * 2}, {workspace, (int64_t)workspace_bytes}};
+  st = check_overlap(in, 2, out, 2);
+  if (st != LMHEAD_OK) return st;
+  if ((H + lmh::kSumCols - 1) / lmh::kSumCols > 65535) return LMHEAD_ERR_SHAPE;  // grid rows
+  st = current_device(&dev);
+  if (st != LMHEAD_OK) return st;
+  const EmbedPlan e = embed_plan(tokens, V);
+  Carver c(workspace);
+  const EmbedScratch s = carve_embed(c, e, tokens, H);
+  return cleared(run_embed_grad(dev, d_out, dtype, ids, tokens, V, v_begin, H, scale, d_W,
+                                accumulate, e, s, stream));
 }
 
 }  // extern "C"

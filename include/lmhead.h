@@ -339,6 +339,38 @@ int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64
                               void* d_hidden, void* d_W, void* d_bias, int accumulate,
                               void* workspace, size_t workspace_bytes, lmhead_stream_t stream);
 
+/*
+ * Token embedding from a table of W's layout (the head's own W, when the two are tied).
+ *   out[t] = round(scale * W[ids[t] - v_begin])       one fp32 multiply, rounded once to dtype
+ * An id outside [v_begin, v_begin + V) gives a row of zeros: a table split over GPUs by vocabulary
+ * (each holds W[v_begin, v_begin + V)) gives the embedding as the sum of the GPUs' results, and a
+ * negative id stands for no token. The plain table has v_begin = 0.
+ *
+ * lmhead_embedding_grad is its gradient:
+ *   d_W[v] = round(scale * sum over {t : ids[t] - v_begin == v} of d_out[t])
+ * each row's tokens added in order of t in fp32 (in parts of fixed size where they are many), so
+ * the result is the same on every run. Rows without a token are 0. accumulate != 0 adds to what
+ * d_W holds instead (in fp32, rounded once) and touches only rows with a token: after
+ * lmhead_cross_entropy_grad has written the head's part of a tied table, this adds the embedding's.
+ * What d_out holds for ids outside the table reaches nothing.
+ *
+ *   ids      int32 [tokens], 4-byte aligned           tokens >= 0
+ *   W, d_W   dtype [V, H], 16-byte aligned            H > 0, H % 8 == 0, V > 0
+ *   out, d_out  dtype [tokens, H], 16-byte aligned    v_begin >= 0, v_begin + V <= 2^31
+ *   workspace   at least lmhead_embedding_grad_workspace_bytes(tokens, V, H) bytes, 256-byte aligned
+ *   tokens, H, V < 2^30
+ * Outputs and the workspace must not overlap each other or the inputs. The first enqueues one
+ * kernel, the second two or three (tokens == 0 writes zeros, or nothing when it accumulates). Each
+ * returns an lmhead_status.
+ */
+int lmhead_embedding(const int32_t* ids, int64_t tokens, const void* W, int dtype, int64_t V,
+                     int64_t v_begin, int64_t H, float scale, void* out, lmhead_stream_t stream);
+size_t lmhead_embedding_grad_workspace_bytes(int64_t tokens, int64_t V, int64_t H);
+int lmhead_embedding_grad(const void* d_out, int dtype, const int32_t* ids, int64_t tokens,
+                          int64_t V, int64_t v_begin, int64_t H, float scale, void* d_W,
+                          int accumulate, void* workspace, size_t workspace_bytes,
+                          lmhead_stream_t stream);
+
 /* A static English description of a status code. Never NULL. */
 const char* lmhead_status_string(int status);
 

@@ -124,3 +124,34 @@ def assert_close(got, want, tol, what):
             f"{what}: {int(bad.sum())} of {bad.numel()} outside the bound; worst at "
             f"{tuple(int(i) for i in at)}: {float(got.reshape(-1)[worst])!r} for "
             f"{float(want.reshape(-1)[worst])!r}, bound {float(tol.reshape(-1)[worst])!r}")
+
+
+def embedding(ids, W, scale=1.0, v_begin=0):
+    """(rows, bound): one fp32 multiply and one rounding."""
+    local = ids.long() - v_begin
+    held = (local >= 0) & (local < W.shape[0])
+    rows = W.double()[local.clamp(0, W.shape[0] - 1)] * scale
+    rows = torch.where(held[..., None], rows, 0.0)
+    u = half_step(W.dtype)
+    return rows, (u + 2.0 ** -23) * rows.abs() + torch.finfo(W.dtype).smallest_normal * u
+
+
+def embedding_grad(d_out, ids, V, scale=1.0, v_begin=0, base=None):
+    """(d_W, bound): an fp32 sum of n terms in any order errs by less than n 2^-24 of the sum of
+    their sizes; then the scale, the base's addition and the rounding to 16 bits."""
+    H = d_out.shape[-1]
+    flat, local = d_out.reshape(-1, H), ids.reshape(-1).long() - v_begin
+    at = ((local >= 0) & (local < V)).nonzero()[:, 0]
+    rows, local = flat[at].double(), local[at]
+    d_W = torch.zeros((V, H), dtype=torch.float64, device=d_out.device)
+    size = torch.zeros_like(d_W)
+    d_W.index_add_(0, local, rows)
+    size.index_add_(0, local, rows.abs())
+    n = torch.bincount(local, minlength=V).double()[:, None]
+    tol = abs(scale) * size * (n + 2) * 2.0 ** -24
+    d_W = d_W * scale
+    if base is not None:
+        d_W = d_W + base.double()
+        tol = tol + 2.0 ** -23 * base.double().abs()
+    u = half_step(d_out.dtype)
+    return d_W, tol + (u + 2.0 ** -23) * d_W.abs() + torch.finfo(d_out.dtype).smallest_normal * u
