@@ -65,7 +65,7 @@ XentPack carve_pack(Carver& c, int64_t rows, int64_t H, bool ignoring) {
 struct XentForward {
   XentPack pack;
   float2* partials;
-  float *target_z, *row_loss;
+  float* row_loss;
 };
 
 int64_t xent_chunks(int64_t V) { return (V + lmh::kXChunk - 1) / lmh::kXChunk; }
@@ -74,7 +74,6 @@ XentForward carve_forward(Carver& c, int64_t rows, int64_t H, int64_t V, bool ig
   XentForward f;
   f.pack = carve_pack(c, rows, H, ignoring);
   f.partials = c.take<float2>(xent_chunks(V) * rows);
-  f.target_z = c.take<float>(rows);
   f.row_loss = c.take<float>(rows);
   return f;
 }
@@ -114,7 +113,7 @@ XentPieces xent_pieces(int64_t rows, int64_t H, int64_t V) {
 struct XentBackward {
   XentPack pack;
   float4* row_info;
-  float* scale;
+  float *lost, *scale;
   uint16_t* d[2];
   float* dh_partial;
 };
@@ -124,6 +123,7 @@ XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_
   XentBackward b;
   b.pack = carve_pack(c, rows, H, ignoring);
   b.row_info = c.take<float4>(rows);
+  b.lost = c.take<float>(rows);
   b.scale = c.take<float>(2);
   b.d[0] = c.take<uint16_t>(x.rows_pad * x.piece);
   b.d[1] = x.n_pieces > 1 ? c.take<uint16_t>(x.rows_pad * x.piece) : b.d[0];
@@ -159,6 +159,30 @@ int encode_xent(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
                 uint32_t box_rows) {
   return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, cols * 2, rows, 128, box_rows,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// The same matrix (cols a multiple of 64) seen as [cols / 64][rows][64], in boxes of 64 rows of
+// `blocks` column blocks.
+int encode_xent_mn(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
+                   uint32_t blocks) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return LMHEAD_ERR_LAUNCH;
+  const int esize = LMHEAD_TMA_WIDE ? 4 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)(128 / esize), (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(cols * 2), 128};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / esize), 64, blocks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      enc(map, LMHEAD_TMA_WIDE ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LMHEAD_OK : LMHEAD_ERR_LAUNCH;
+}
+
+// Rows of B in one CTA's tile.
+uint32_t xent_b_rows(bool pair) {
+  return pair ? lmh::XentTile<true>::kBRows : lmh::XentTile<false>::kBRows;
 }
 
 int launch_xent_gemm(const DeviceInfo& dev, bool fp16, bool pair, const lmh::XentMaps& maps,
@@ -205,16 +229,18 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   int st = current_device(&dev);
   if (st != LMHEAD_OK) return st;
   const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
+  const bool fp16 = dtype == LMHEAD_DTYPE_F16;
   const XentPack& k = f.pack;
   if (ignoring) {
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
     if (st != LMHEAD_OK) return st;
   }
+  const bool pair = xent_pairs(dev, rows);
   lmh::XentMaps maps = {};
   st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
-                   ignoring ? round_up(rows, lmh::kBK) : rows, 64);
+                   ignoring ? round_up(rows, lmh::kBK) : rows, 128);
   if (st != LMHEAD_OK) return st;
-  st = encode_xent(&maps.m[lmh::kMapW], W, H, V, 64);
+  st = encode_xent(&maps.m[lmh::kMapW], W, H, V, xent_b_rows(pair));
   if (st != LMHEAD_OK) return st;
 
   lmh::XentParams p = {};
@@ -224,22 +250,22 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   p.rows = (int32_t)rows;
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
-  p.group = 8;
+  p.group = 16;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
   p.targets = ignoring ? k.targets : targets;
   p.partials = f.partials;
-  p.target_z = f.target_z;
   p.wait = wait_cfg();
-  st = launch_xent_gemm(dev, dtype == LMHEAD_DTYPE_F16, xent_pairs(dev, rows), maps, p, stream);
+  st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
   if (st != LMHEAD_OK) return st;
 
   float* row_loss = reduction == LMHEAD_REDUCE_NONE ? loss : f.row_loss;
-  st = launch_head(lmh::xent_fold_kernel,
+  st = launch_head(fp16 ? lmh::xent_fold_kernel<true> : lmh::xent_fold_kernel<false>,
                    (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows), 1024, 0, stream, 1u,
                    (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
-                   (int32_t)rows, (int32_t)V, (const int32_t*)k.place, p.targets,
-                   (const float*)f.target_z, z_loss, row_loss, lse);
+                   (int32_t)rows, (int32_t)V, (const int32_t*)k.place, targets,
+                   reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
+                   (int32_t)(H / 8), p.bias, alpha, z_loss, row_loss, lse);
   if (st != LMHEAD_OK || reduction == LMHEAD_REDUCE_NONE) return st;
   return launch_head(lmh::xent_reduce_kernel, 1, 1024, 0, stream, 1u, (const float*)row_loss,
                      (int32_t)rows, (const int32_t*)k.n_rows,
@@ -263,21 +289,38 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
     if (st != LMHEAD_OK) return st;
   }
-  const int32_t* tgt = ignoring ? k.targets : targets;
-  st = launch_head(lmh::xent_rows_kernel, 1, 1024, 0, stream, 1u, lse, tgt,
+  int64_t row_blocks = (rows + lmh::kRowsBlock - 1) / lmh::kRowsBlock;
+  if (row_blocks > 2 * dev.num_sms) row_blocks = 2 * dev.num_sms;
+  st = launch_head(fp16 ? lmh::xent_rows_kernel<true> : lmh::xent_rows_kernel<false>,
+                   (unsigned)row_blocks, 1024, 0, stream, 1u, lse, targets,
                    (const int32_t*)k.row_of, (int32_t)rows, (const int32_t*)k.n_rows, (int32_t)V,
-                   grad_loss, (int32_t)(reduction == LMHEAD_REDUCE_NONE),
-                   (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.scale);
+                   reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
+                   (int32_t)(H / 8), reinterpret_cast<const uint16_t*>(bias), grad_loss,
+                   (int32_t)(reduction == LMHEAD_REDUCE_NONE),
+                   (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.lost, b.scale);
   if (st != LMHEAD_OK) return st;
 
+  // the forms of hidden and W as B's MN-major operand: in 3-D boxes, or where H is no multiple of
+  // 64, in 2-D ones of 64 x 64
+  const bool flat = H % 64 != 0;
+  const uint32_t b_rows = xent_b_rows(pair);
+  const void* h = ignoring ? k.hidden : hidden;
+  const int64_t h_rows = ignoring ? round_up(rows, lmh::kBK) : rows;
   lmh::XentMaps maps = {};
-  st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
-                   ignoring ? round_up(rows, lmh::kBK) : rows, 64);
-  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, 64);
+  st = encode_xent(&maps.m[lmh::kMapHidden], h, H, h_rows, 128);
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, b_rows);
+  if (st == LMHEAD_OK)
+    st = flat ? encode_xent(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, 64)
+              : encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, b_rows / 64);
+  if (st == LMHEAD_OK)
+    st = flat ? encode_xent(&maps.m[lmh::kMapWMn], W, H, V, 64)
+              : encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, b_rows / 64);
   for (int i = 0; i < 2 && st == LMHEAD_OK; ++i) {
-    st = encode_xent(&maps.m[lmh::kMapD0 + i], b.d[i], x.piece, x.rows_pad, 64);
+    st = encode_xent(&maps.m[lmh::kMapD + i], b.d[i], x.piece, x.rows_pad, 128);
     if (st == LMHEAD_OK)
-      st = encode_xent(&maps.m[lmh::kMapD0Store + i], b.d[i], x.piece, x.rows_pad, 32);
+      st = encode_xent_mn(&maps.m[lmh::kMapDMn + i], b.d[i], x.piece, x.rows_pad, 2);
+    if (st == LMHEAD_OK)
+      st = encode_xent(&maps.m[lmh::kMapDStore + i], b.d[i], x.piece, x.rows_pad, 32);
   }
   if (st == LMHEAD_OK && d_W != nullptr) st = encode_xent(&maps.m[lmh::kMapDw], d_W, H, V, 32);
   if (st != LMHEAD_OK) return st;
@@ -287,10 +330,9 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
   p.rows_pad = (int32_t)x.rows_pad;
-  p.group = 8;
+  p.group = 16;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
-  p.targets = tgt;
   p.row_info = b.row_info;
   p.scale = b.scale;
   p.d_weight = reinterpret_cast<uint16_t*>(d_W);
@@ -304,14 +346,13 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
         xent_problem(lmh::kXentDlogits, lmh::kMapHidden, lmh::kMapW, length(c), H);
     q.m_rows = 1;
     q.b_off = (int32_t)start(c);
-    q.out_map = lmh::kMapD0Store + (c & 1);
+    q.out_map = lmh::kMapDStore + (c & 1);
     return q;
   };
   p.n_problems = 1;
   p.prob[0] = logits_of(0);
   st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
   for (int c = 0; c < x.n_pieces && st == LMHEAD_OK; ++c) {
-    const int d_map = lmh::kMapD0 + (c & 1);
     if (d_bias != nullptr) {
       const unsigned blocks = (unsigned)((length(c) + lmh::kBiasCols - 1) / lmh::kBiasCols);
       st = launch_head(fp16 ? lmh::xent_bias_kernel<true> : lmh::xent_bias_kernel<false>, blocks,
@@ -323,9 +364,11 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     }
     p.n_problems = 0;
     if (d_hidden != nullptr) {  // the longest tiles first
-      lmh::XentProblem q = xent_problem(lmh::kXentDhidden, d_map, lmh::kMapW, H, length(c));
+      lmh::XentProblem q = xent_problem(lmh::kXentDhidden, lmh::kMapD + (c & 1),
+                                         lmh::kMapWMn, H, length(c));
       q.m_rows = 1;
       q.b_mn = 1;
+      q.b_flat = flat;
       q.b_off = (int32_t)start(c);
       q.b_k = 1;
       q.splits = x.splits;
@@ -333,10 +376,12 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
       p.prob[p.n_problems++] = q;
     }
     if (d_W != nullptr) {
-      lmh::XentProblem q = xent_problem(lmh::kXentDweight, d_map, lmh::kMapHidden, H, 0);
+      lmh::XentProblem q = xent_problem(lmh::kXentDweight, lmh::kMapDMn + (c & 1),
+                                         lmh::kMapHiddenMn, H, 0);
       q.m_len = (int32_t)length(c);
       q.k_rows = 1;
       q.a_mn = q.b_mn = 1;
+      q.b_flat = flat;
       q.out_off = (int32_t)start(c);
       q.out_map = lmh::kMapDw;
       q.add = accumulate != 0;
@@ -350,8 +395,10 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   return launch_head(
       fp16 ? lmh::xent_finish_hidden_kernel<true> : lmh::xent_finish_hidden_kernel<false>,
       (unsigned)((vecs + lmh::kFinishThreads - 1) / lmh::kFinishThreads), lmh::kFinishThreads, 0,
-      stream, 1u, (const float*)b.dh_partial, x.splits, x.rows_pad * H, (int32_t)rows, (int32_t)H,
-      (const int32_t*)k.place, (const float*)b.scale, reinterpret_cast<uint4*>(d_hidden));
+      stream, 1u, (const float*)b.dh_partial, x.splits, x.rows_pad * H, (int32_t)rows,
+      (int32_t)(H / 8), (const int32_t*)k.place, targets, (int32_t)V, (const float*)b.lost,
+      reinterpret_cast<const uint4*>(W), (const float*)b.scale,
+      reinterpret_cast<uint4*>(d_hidden));
 }
 
 int cleared(int st) {

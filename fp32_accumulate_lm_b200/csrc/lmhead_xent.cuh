@@ -40,8 +40,8 @@
 // and what they hold (NaN of padding) never meets a product. The number of rows that count is known
 // on the device only; the tile walk reads it there.
 //
-// Roles as in the fp32 head: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue; tiles by cluster launch
-// control in launch order. No atomics on data and no split whose order varies: results are the
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue, warp 10 tile scheduler (cluster launch
+// control, in launch order). No atomics on data and no split whose order varies: results are the
 // same on every run.
 #pragma once
 
@@ -50,9 +50,10 @@
 namespace lmh {
 
 constexpr int kXN = 256;                  // tile columns (MMA N)
-constexpr int kXBox = 64 * 64 * 2;        // bytes of one TMA box: 64 rows of 64 16-bit elements
+constexpr int kXBlock = 64 * 64 * 2;      // bytes of 64 K rows of 64 entries of M or N
 constexpr int kXEpiWarps = 8;
-constexpr int kXThreads = 64 + 32 * kXEpiWarps;
+constexpr int kXThreads = 64 + 32 * kXEpiWarps + 32;
+constexpr int kXInfoSlots = 2;            // tiles the scheduler warp announces ahead
 constexpr int kXStoreBox = 32 * 64 * 2;   // an epilogue warp's store box: 32 rows of 64 elements
 constexpr int kXMaxProblems = 3;
 constexpr int kXChunk = 128;              // vocab entries per (max, sum) pair of a row
@@ -71,22 +72,29 @@ struct XentTile {
 };
 
 enum : int32_t {
-  kXentStats = 0,    // (max, sum of exp(z - max)) per row and 128 vocab entries, the target's logit
+  kXentStats = 0,    // (max, sum) per row and 128 vocab entries, the target left out
   kXentDlogits = 1,  // d, 16 bits, [rows, ld] of one vocab piece
   kXentDweight = 2,  // dW rows, 16 bits, optionally added to what is there
   kXentDhidden = 3,  // fp32 partial sums of dH, one buffer per split of K
 };
 
-// Tensor maps of one launch, all of them 2-D with 128-byte swizzle.
+// Tensor maps of one launch, all of them with 128-byte swizzle. A K-major operand is a 2-D matrix in
+// boxes of 64 columns by all rows of a CTA's tile (128 of A, kBRows of B). An MN-major one comes as
+// a 3-D view [columns / 64][rows][64], a box being 64 rows of every 64-column block of the CTA's
+// tile. One box a stage and operand either way: with 64 x 64 boxes, two to four of them, the same
+// loads fed the tensor cores at 1150 TFLOP/s and not at 1325 (8192 x 4096 x 128256 logits under
+// the power cap). Where H is no multiple of 64 the 3-D view of hidden and W does not exist, and
+// their MN-major tiles come as 64 x 64 boxes of the 2-D matrix.
 enum : int32_t {
-  kMapHidden = 0,  // [rows, H], boxes of 64 rows
-  kMapW = 1,       // [V, H], boxes of 64 rows
-  kMapD0 = 2,      // d buffers [rows_pad, ld], boxes of 64 rows (loads)
-  kMapD1 = 3,
-  kMapD0Store = 4,  // the same with boxes of 32 rows (stores)
-  kMapD1Store = 5,
-  kMapDw = 6,      // dW [V, H], boxes of 32 rows (stores)
-  kMapCount = 7,
+  kMapHidden = 0,    // [rows, H], K-major
+  kMapHiddenMn = 1,  // [rows, H], MN-major
+  kMapW = 2,         // [V, H], K-major
+  kMapWMn = 3,       // [V, H], MN-major
+  kMapD = 4,         // the two d buffers [rows_pad, piece], K-major
+  kMapDMn = 6,       // the same, MN-major
+  kMapDStore = 8,    // the same in boxes of 32 rows (stores)
+  kMapDw = 10,       // dW [V, H] in boxes of 32 rows (stores)
+  kMapCount = 11,
 };
 struct XentMaps {
   CUtensorMap m[kMapCount];
@@ -95,11 +103,12 @@ struct XentMaps {
 struct XentProblem {
   int32_t kind;
   int32_t a_map, b_map, out_map;
-  int32_t a_mn, b_mn;     // 1: the operand's K runs down the rows of its matrix
+  int32_t a_mn, b_mn;     // 1: the operand is MN-major (its K runs down the rows of its matrix)
+  int32_t b_flat;         // 1: an MN-major B comes as 2-D boxes
   int32_t m_rows;         // 1: M is the number of rows that count (else m_len)
   int32_t k_rows;         // 1: K is the number of rows that count (else k_len)
   int32_t m_len, n_len, k_len;
-  int32_t a_off, b_off;   // first row of the operand's matrix (a piece of W starts at vocab b_off)
+  int32_t b_off;          // first row of B's matrix (a piece of W starts at vocab entry b_off)
   int32_t b_k;            // 1: b_off is along K (dH: the piece's rows of W are B's K)
   int32_t splits;         // of K
   int32_t out_off;        // first output row (dW: the piece's first vocab entry)
@@ -118,8 +127,7 @@ struct XentParams {
   const uint16_t* bias;       // [V] or null
   const int32_t* targets;     // [rows that count]
   float2* partials;           // stats: [2 * ceil(V / 256)][rows]
-  float* target_z;            // stats: [rows that count]
-  const float4* row_info;     // dlogits: (lse, a, b, target as int bits) of each row that counts
+  const float4* row_info;     // dlogits: (lse * log2(e), a, d at the target, target as int bits)
   const float* scale;         // device: [1] = the factor of the gradients
   uint16_t* d_weight;         // dW as memory, for add
   float* dh_partial;          // [splits][rows_pad][H]
@@ -141,27 +149,130 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// As mma_bf16_ss_elect for a CTA pair (issued by the even CTA only).
-__device__ __forceinline__ void mma_bf16_ss_pair_elect(uint32_t d_tmem, uint64_t a_desc,
-                                                       uint64_t b_desc, uint32_t idesc,
-                                                       uint32_t accumulate) {
+// The TMEM loads issued so far have arrived; `r`, the last of them, is used behind this only.
+__device__ __forceinline__ void tmem_ld_wait_x32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Pairs of fp32 values in one instruction (each half rounds as the scalar instruction does).
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// One K step of 64 (four K = 16 MMAs, M rows across the pair for a pair) from a converged warp, one
+// elected lane issuing; the operands advance by their own steps, in 16-byte units. Only the first
+// MMA may start a fresh accumulator.
+template <bool kPair>
+__device__ __forceinline__ void mma4_f16_steps_elect(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                                     uint64_t a_step, uint64_t b_step,
+                                                     uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 a2, a1, %5;\n\tadd.s64 a3, a2, %5;\n\t"
+        "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "l"(a_step), "l"(b_step)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 a2, a1, %5;\n\tadd.s64 a3, a2, %5;\n\t"
+        "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "l"(a_step), "l"(b_step)
+        : "memory");
+  }
+}
+
+// Shared-memory descriptor of an MN-major tile in 64 x 64 blocks: each block is 64 K rows of 128
+// bytes (64 entries of M or N, 128-byte swizzle), 8 K rows make an atom of 1024 bytes (the stride
+// offset), the next 64 entries of M or N are the next block (the leading offset).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
+  const uint64_t start = (smem_addr & 0x3FFFFu) >> 4;
+  const uint64_t lbo = (uint32_t)kXBlock >> 4;
+  const uint64_t sbo = 1024u >> 4;
+  return start | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// As tma_load_2d_pair, from a 3-D view.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar, int32_t x, int32_t y, int32_t z,
+                                                 uint64_t policy) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(pair_leader_addr(bar)), "r"(x), "r"(y), "r"(z),
+      "l"(policy)
       : "memory");
 }
 
-// Shared-memory descriptor of an MN-major tile in 64 x 64 boxes: each box is 64 K rows of 128
-// bytes (64 entries of M or N, 128-byte swizzle), 8 K rows make an atom of 1024 bytes (the stride
-// offset), the next 64 entries of M or N are the next box (the leading offset).
-__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
-  const uint64_t start = (smem_addr & 0x3FFFFu) >> 4;
-  const uint64_t lbo = (uint32_t)kXBox >> 4;
-  const uint64_t sbo = 1024u >> 4;
-  return start | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+template <bool kPair>
+__device__ __forceinline__ void xent_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                             int32_t col, int32_t row, uint64_t policy) {
+  if constexpr (kPair)
+    tma_load_2d_pair(dst, map, bar, tma_x((int64_t)col * 2, 2), row, policy);
+  else
+    tma_load_2d(dst, map, bar, tma_x((int64_t)col * 2, 2), row, policy);
+}
+// `col` is a multiple of 64: the block is its own coordinate.
+template <bool kPair>
+__device__ __forceinline__ void xent_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                             int32_t col, int32_t row, uint64_t policy) {
+  if constexpr (kPair)
+    tma_load_3d_pair(dst, map, bar, 0, row, col / 64, policy);
+  else
+    tma_load_3d(dst, map, bar, 0, row, col / 64, policy);
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x,
@@ -218,113 +329,215 @@ struct XentTileAt {
 
 __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
 
-// Tile t of the launch: the problems one after another, each split by split, M tiles in groups
-// walked N-major (a wave of tiles is then about as high as wide, and its operands fit L2).
+// The launch's tiles: the problems one after another, each split by split, M tiles in groups walked
+// N-major (a wave of tiles is then about as high as wide, and its operands fit L2). What does not
+// depend on the tile is worked out once: a tile's coordinates cost three 32-bit divisions.
 template <int kM>
-__device__ __forceinline__ XentTileAt xent_tile(const XentParams& p, int32_t n_rows, int32_t t) {
-  XentTileAt c;
-  c.prob = -1;
-  c.m0 = c.n0 = c.k0 = c.k_steps = c.split = 0;
+struct XentWalk {
+  int32_t mt[kXMaxProblems], nt[kXMaxProblems], ks[kXMaxProblems];
+
+  __device__ __forceinline__ XentWalk(const XentParams& p, int32_t n_rows) {
 #pragma unroll
-  for (int i = 0; i < kXMaxProblems; ++i) {
-    if (i >= p.n_problems) break;
-    const XentProblem& q = p.prob[i];
-    const int32_t mt = ceil_div(q.m_rows ? n_rows : q.m_len, kM);
-    const int32_t nt = ceil_div(q.n_len, kXN);
-    const int32_t per = mt * nt, count = per * q.splits;
-    if (t < count) {
-      const int32_t split = t / per;
-      const int32_t u = t - split * per;
-      const int32_t g = u / (p.group * nt);
-      const int32_t local = u - g * p.group * nt;
-      const int32_t gm = min(p.group, mt - g * p.group);
-      const int32_t n = local / gm;
-      c.prob = i;
-      c.m0 = (g * p.group + (local - n * gm)) * kM;
-      c.n0 = n * kXN;
-      c.split = split;
-      const int32_t ks = ceil_div(q.k_rows ? n_rows : q.k_len, kBK);
-      c.k0 = (int32_t)((int64_t)ks * split / q.splits);
-      c.k_steps = (int32_t)((int64_t)ks * (split + 1) / q.splits) - c.k0;
-      return c;
+    for (int i = 0; i < kXMaxProblems; ++i) {
+      const XentProblem& q = p.prob[i];
+      const bool used = i < p.n_problems;
+      mt[i] = used ? ceil_div(q.m_rows ? n_rows : q.m_len, kM) : 0;
+      nt[i] = used ? ceil_div(q.n_len, kXN) : 0;
+      ks[i] = used ? ceil_div(q.k_rows ? n_rows : q.k_len, kBK) : 0;
     }
-    t -= count;
   }
-  return c;
+
+  __device__ __forceinline__ XentTileAt at(const XentParams& p, int32_t t) const {
+    XentTileAt c;
+    c.prob = -1;
+    c.m0 = c.n0 = c.k0 = c.k_steps = c.split = 0;
+#pragma unroll
+    for (int i = 0; i < kXMaxProblems; ++i) {
+      const uint32_t per = (uint32_t)(mt[i] * nt[i]);
+      const int32_t splits = p.prob[i].splits;
+      if (c.prob < 0 && t >= 0) {
+        if (t < (int32_t)per * splits) {
+          const uint32_t split = splits == 1 ? 0u : (uint32_t)t / per;
+          const uint32_t u = (uint32_t)t - split * per;
+          const uint32_t group_tiles = (uint32_t)(p.group * nt[i]);
+          const uint32_t g = u / group_tiles;
+          const uint32_t local = u - g * group_tiles;
+          const uint32_t gm = (uint32_t)min(p.group, mt[i] - (int32_t)g * p.group);
+          const uint32_t n = local / gm;
+          c.prob = i;
+          c.m0 = ((int32_t)g * p.group + (int32_t)(local - n * gm)) * kM;
+          c.n0 = (int32_t)n * kXN;
+          c.split = (int32_t)split;
+          // (at most 2^24 steps by 32 splits)
+          c.k0 = splits == 1 ? 0 : (int32_t)((uint32_t)ks[i] * split / (uint32_t)splits);
+          c.k_steps = (splits == 1 ? ks[i]
+                                   : (int32_t)((uint32_t)ks[i] * (split + 1) / (uint32_t)splits)) -
+                      c.k0;
+        }
+        t -= (int32_t)per * splits;
+      }
+    }
+    return c;
+  }
+};
+
+// The tiles of a CTA as its scheduler warp announces them to the other roles. That warp asks for
+// tiles by cluster launch control, takes the answers and works out the coordinates, a tile ahead:
+// done by the MMA warp itself, between two tiles, this took 1000 clocks a tile in which nothing
+// was issued.
+struct XentInfo {
+  uint32_t slot0, full0, empty0;
+};
+
+__device__ __forceinline__ bool xent_announce(const XentInfo& f, int j, const XentTileAt& c,
+                                              bool last, const WaitCfg& w,
+                                              volatile int* abort_flag) {
+  const int k = j % kXInfoSlots;
+  if (!wait_bounded(f.empty0 + 8 * k, ((uint32_t)(j / kXInfoSlots) & 1u) ^ 1u, w, abort_flag,
+                    kSleepHintNs))
+    return false;
+  if ((threadIdx.x & 31) == 0) {
+    st_shared_v4(f.slot0 + 32 * k, last ? 0xfffffffeu : (uint32_t)c.prob, (uint32_t)c.m0,
+                 (uint32_t)c.n0, (uint32_t)c.k0);
+    st_shared_v4(f.slot0 + 32 * k + 16, (uint32_t)c.k_steps, (uint32_t)c.split, 0u, 0u);
+    mbar_arrive(f.full0 + 8 * k);
+  }
+  __syncwarp();
+  return true;
+}
+
+// Tile j, by a whole warp. prob is -1 where there is nothing to do and -2 behind the last tile.
+__device__ __forceinline__ bool xent_read(const XentInfo& f, int j, XentTileAt& c,
+                                          const WaitCfg& w, volatile int* abort_flag,
+                                          uint32_t sleep_ns = 0) {
+  const int k = j % kXInfoSlots;
+  if (!wait_bounded(f.full0 + 8 * k, (uint32_t)(j / kXInfoSlots) & 1u, w, abort_flag, sleep_ns))
+    return false;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(c.prob), "=r"(c.m0), "=r"(c.n0), "=r"(c.k0)
+               : "r"(f.slot0 + 32 * k)
+               : "memory");
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+               : "=r"(c.k_steps), "=r"(c.split)
+               : "r"(f.slot0 + 32 * k + 16)
+               : "memory");
+  // the same in every lane, and the compiler may know it
+  c.prob = __shfl_sync(0xffffffffu, c.prob, 0);
+  c.k_steps = __shfl_sync(0xffffffffu, c.k_steps, 0);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(f.empty0 + 8 * k);
+  __syncwarp();
+  return true;
 }
 
 // ------------------------------------------------------------------ epilogues
 // Each is called by one warp with its 32 rows of the tile (row = its lane's) and its 128 columns
 // from `col`; `tacc` addresses the first of them in TMEM; `zero` says that K was empty and the
-// accumulator was never written.
+// accumulator was never written. Columns come 32 at a time. The two softmax epilogues work in units of log 2 (z * log2(e), one multiply for
+// alpha and the change of base) on pairs of values: at 1024-wide hidden rows a tile's MMAs take
+// about 8000 clocks and 128 x 256 exponentials 2000 of the SM's special-function unit, but one
+// instruction at a time (some 18 an entry) the epilogue took 15000 and held the tensor pipe up.
 
-__device__ __forceinline__ void xent_acc32(uint32_t tacc, bool zero, uint32_t (&r)[32]) {
+__device__ __forceinline__ void xent_acc_load(uint32_t tacc, bool zero, uint32_t (&r)[32]) {
   __syncwarp();  // the lanes may come from rows of their own; the TMEM load is the warp's
   if (zero) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) r[j] = 0u;
   } else {
     tmem_ld_32x32b_x32(tacc, r);
-    tmem_ld_wait();
   }
 }
 
-// Lane's own column of 32: the bias of vocab entry v0 + lane (0 past the end or without a bias).
+// Calls step(c, r) for the column groups c = 0, 32, 64, 96 that begin before `cols`. (One group at a
+// time: the two warps that share a scheduler cover each other's TMEM loads, and a second buffer of
+// 32 registers spilled.)
+template <typename Step>
+__device__ __forceinline__ void xent_columns(uint32_t tacc, bool zero, int32_t cols, Step step) {
+#pragma unroll 1
+  for (int c = 0; c < kXChunk && c < cols; c += 32) {
+    uint32_t r[32];
+    xent_acc_load(tacc + (uint32_t)c, zero, r);
+    tmem_ld_wait_x32(r);
+    step(c, r);
+  }
+}
+
+// Lane's own column of 32: the bias of vocab entry v0 + lane (0 past the end), times `factor`.
 template <bool kF16>
-__device__ __forceinline__ float xent_bias(const XentParams& p, int32_t v0, int32_t v_end) {
+__device__ __forceinline__ float xent_bias(const XentParams& p, int32_t v0, int32_t v_end,
+                                           float factor) {
   const int32_t v = v0 + (int)(threadIdx.x & 31);
-  return p.bias != nullptr && v < v_end ? unpack16<kF16>(p.bias[v]) : 0.0f;
+  return v < v_end ? unpack16<kF16>(p.bias[v]) * factor : 0.0f;
 }
 
-__device__ __forceinline__ float xent_logit(const XentParams& p, uint32_t acc, float bias_lane,
-                                            int j) {
-  const float a = __uint_as_float(acc);
-  return p.bias == nullptr
-             ? __fmul_rn(p.alpha, a)
-             : __fmul_rn(p.alpha, __fadd_rn(a, __shfl_sync(0xffffffffu, bias_lane, j)));
+// x[j] = acc[j] * factor + shift (+ bias * factor), in pairs.
+template <bool kF16>
+__device__ __forceinline__ void xent_scaled(const XentParams& p, uint32_t (&r)[32], float factor,
+                                            float shift, int32_t v0, int32_t v_end) {
+  const uint64_t f2 = pair_f32(factor, factor), s2 = pair_f32(shift, shift);
+  if (p.bias == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      float lo, hi;
+      unpair_f32(fma2(pair_f32(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2, s2), lo, hi);
+      r[j] = __float_as_uint(lo);
+      r[j + 1] = __float_as_uint(hi);
+    }
+  } else {
+    const float b = xent_bias<kF16>(p, v0, v_end, factor);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const uint64_t b2 = pair_f32(__shfl_sync(0xffffffffu, b, j), __shfl_sync(0xffffffffu, b, j + 1));
+      float lo, hi;
+      unpair_f32(fma2(pair_f32(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2, add2(b2, s2)),
+                 lo, hi);
+      r[j] = __float_as_uint(lo);
+      r[j + 1] = __float_as_uint(hi);
+    }
+  }
 }
 
-// (max, sum of exp(z - max)) of this thread's row over its 128 vocab entries, and the target's
-// logit if it is one of them. Per 32 entries: their maximum first, one rescaling of the running
-// sum, then the terms. Entries past V count as -inf; a row of -inf alone gives (-inf, 0).
+// (max, sum of 2^(x - max)) of this thread's row over its 128 vocab entries, x = z * log2(e), the
+// target left out: its logit is taken exactly later (see xent_target_logit). Per 32 entries: their
+// maximum first, one rescaling of the running sum, then the terms. Entries past V and the target
+// count as -inf; -inf alone gives (-inf, 0). A NaN logit reaches the sum through its own term;
+// +inf gives inf - inf there, NaN as well.
 template <bool kF16>
 __device__ __forceinline__ void xent_epi_stats(const XentParams& p, const XentProblem& q,
                                                uint32_t tacc, bool zero, int32_t row, bool row_ok,
-                                               int32_t col) {
+                                               int32_t t, int32_t col) {
   const int32_t V = q.n_len;
-  const int32_t t = row_ok ? p.targets[row] : -1;
   float m = -INFINITY, s = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < kXChunk && col + c < V; c += 32) {
-    uint32_t r[32];
-    xent_acc32(tacc + (uint32_t)c, zero, r);
+  xent_columns(tacc, zero, V - col, [&](int c, uint32_t(&r)[32]) {
     const int32_t v0 = col + c;
-    const float b = xent_bias<kF16>(p, v0, V);
-    float cm = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      float z = xent_logit(p, r[j], b, j);
-      if (v0 + j >= V) z = -INFINITY;
-      r[j] = __float_as_uint(z);
-      cm = fmaxf(cm, z);
-    }
-    if (__any_sync(0xffffffffu, t >= v0 && t < v0 + 32)) {
+    xent_scaled<kF16>(p, r, p.alpha * kLog2e, 0.0f, v0, V);
+    if (v0 + 32 > V || __any_sync(0xffffffffu, t >= v0 && t < v0 + 32)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (v0 + j == t && t < V) p.target_z[row] = __uint_as_float(r[j]);
+        if (v0 + j >= V || v0 + j == t) r[j] = __float_as_uint(-INFINITY);
     }
-    const float nm = fmaxf(m, cm);
-    const float ref = nm == -INFINITY ? 0.0f : nm;
-    // a NaN logit reaches the sum through its own term; +inf gives inf - inf there, NaN as well
-    float s0 = 0.0f, s1 = 0.0f;
+    float nm = m, m1 = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      s0 += __expf(__uint_as_float(r[j]) - ref);
-      s1 += __expf(__uint_as_float(r[j + 1]) - ref);
+    for (int j = 0; j < 32; j += 4) {
+      nm = max3(nm, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+      m1 = max3(m1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
     }
-    s = s * __expf(m - ref) + (s0 + s1);
+    nm = fmaxf(nm, m1);
+    const float ref = nm == -INFINITY ? 0.0f : nm;
+    const uint64_t neg = pair_f32(-ref, -ref);
+    uint64_t s0 = pair_f32(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float a0, a1, b0, b1;
+      unpair_f32(add2(pair_f32(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), neg), a0, a1);
+      unpair_f32(add2(pair_f32(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), neg), b0, b1);
+      s0 = add2(s0, pair_f32(exp2_approx(a0), exp2_approx(a1)));
+      s1 = add2(s1, pair_f32(exp2_approx(b0), exp2_approx(b1)));
+    }
+    float lo, hi;
+    unpair_f32(add2(s0, s1), lo, hi);
+    s = s * exp2_approx(m - ref) + (lo + hi);
     m = nm;
-  }
+  });
   if (row_ok && col < V)
     __stcs(p.partials + (int64_t)(col / kXChunk) * p.rows + row, make_float2(m, s));
 }
@@ -354,45 +567,54 @@ struct XentStage {
   }
 };
 
+template <bool kF16>
+__device__ __forceinline__ void xent_pack32(const uint32_t (&r)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    w[j] = pack16<kF16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+}
+
 // d of this thread's row over its 128 vocab entries of the piece, 16 bits, into the piece's buffer.
 // Rows that do not count and entries past V are written as 0: the products that read d take whole
-// 64-wide steps.
+// 64-wide steps. The target's entry comes ready with the row's factors.
 template <bool kF16>
 __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t row0,
-                                                 int32_t row, bool row_ok, int32_t col) {
+                                                 bool row_ok, const float4& info, int32_t col) {
   const int32_t V = q.b_off + q.n_len;  // the end of the piece as vocab ids
-  float4 info = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
-  if (row_ok) info = p.row_info[row];
   const int32_t t = __float_as_int(info.w);
-#pragma unroll 1
-  for (int c = 0; c < kXChunk && col + c < q.n_len; c += 64) {
-    st.begin();
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t r[32], w[16];
-      xent_acc32(tacc + (uint32_t)(c + 32 * h), zero, r);
-      const int32_t v0 = q.b_off + col + c + 32 * h;
-      const float b = xent_bias<kF16>(p, v0, V);
+  const uint64_t a2 = pair_f32(info.y, info.y);
+  const bool all_ok = __all_sync(0xffffffffu, row_ok);
+  // (whole boxes of 64 columns: what lies past the piece's end is 0)
+  const int32_t cols = min(kXChunk, (q.n_len - col + 63) / 64 * 64);
+  xent_columns(tacc, zero, cols, [&](int c, uint32_t(&r)[32]) {
+    const int32_t v0 = q.b_off + col + c;
+    xent_scaled<kF16>(p, r, p.alpha * kLog2e, -info.x, v0, V);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float z = xent_logit(p, r[j], b, j);
-        const float d = info.y * __expf(z - info.x);
-        r[j] = row_ok && v0 + j < V ? __float_as_uint(d) : 0u;
-      }
-      if (__any_sync(0xffffffffu, t >= v0 && t < v0 + 32)) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (v0 + j == t) r[j] = __float_as_uint(__uint_as_float(r[j]) - info.z);
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = pack16<kF16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      st.put(h, w);
+    for (int j = 0; j < 32; j += 2) {
+      float lo, hi;
+      unpair_f32(mul2(pair_f32(exp2_approx(__uint_as_float(r[j])),
+                               exp2_approx(__uint_as_float(r[j + 1]))), a2), lo, hi);
+      r[j] = __float_as_uint(lo);
+      r[j + 1] = __float_as_uint(hi);
     }
-    st.store(&maps.m[q.out_map], col + c, row0);
-  }
+    if (__any_sync(0xffffffffu, t >= v0 && t < v0 + 32)) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (v0 + j == t) r[j] = __float_as_uint(info.z);
+    }
+    if (!all_ok || v0 + 32 > V) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!row_ok || v0 + j >= V) r[j] = 0u;
+    }
+    uint32_t w[16];
+    xent_pack32<kF16>(r, w);
+    if ((c & 32) == 0) st.begin();
+    st.put((c >> 5) & 1, w);
+    if (c & 32) st.store(&maps.m[q.out_map], col + c - 32, row0);
+  });
 }
 
 // dW of this thread's vocab entry: the sum times `scale`, added in fp32 to what is there if asked
@@ -402,47 +624,36 @@ __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const Xent
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t row0,
                                                  int32_t row, int32_t col) {
-  const float scale = p.scale[1];
-  const bool row_ok = row < q.m_len;
+  const float scale = zero ? 0.0f : p.scale[1];  // (no row counts: 0, whatever the scale is)
+  const bool add_row = q.add && row < q.m_len;
   const int64_t at = (int64_t)(q.out_off + row) * p.H;
-#pragma unroll 1
-  for (int c = 0; c < kXChunk && col + c < p.H; c += 64) {
-    st.begin();
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t r[32], w[16];
-      const int32_t x = col + c + 32 * h;
-      xent_acc32(tacc + (uint32_t)(c + 32 * h), zero, r);
+  const int32_t cols = min(kXChunk, (p.H - col + 63) / 64 * 64);
+  xent_columns(tacc, zero, cols, [&](int c, uint32_t(&r)[32]) {
+    const int32_t x = col + c;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
-      // nothing to add where no row counts: 0 times a scale that may be NaN stays 0
-      if (zero) {
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
+    if (add_row) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = 0u;
-      }
-      if (q.add && row_ok) {
+      for (int j = 0; j < 4; ++j) {
+        if (x + 8 * j < p.H) {  // H is a multiple of 8
+          const uint4 old = *reinterpret_cast<const uint4*>(p.d_weight + at + x + 8 * j);
+          const uint32_t o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (x + 8 * j < p.H) {  // H is a multiple of 8
-            const uint4 old = *reinterpret_cast<const uint4*>(p.d_weight + at + x + 8 * j);
-            const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 8 * j + 2 * i;
-              r[e] = __float_as_uint(__uint_as_float(r[e]) + unpack16<kF16>(o[i] & 0xffffu));
-              r[e + 1] = __float_as_uint(__uint_as_float(r[e + 1]) + unpack16<kF16>(o[i] >> 16));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int e = 8 * j + 2 * i;
+            r[e] = __float_as_uint(__uint_as_float(r[e]) + unpack16<kF16>(o[i] & 0xffffu));
+            r[e + 1] = __float_as_uint(__uint_as_float(r[e + 1]) + unpack16<kF16>(o[i] >> 16));
           }
         }
       }
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j] = pack16<kF16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      st.put(h, w);
     }
+    uint32_t w[16];
+    xent_pack32<kF16>(r, w);
+    if ((c & 32) == 0) st.begin();
+    st.put((c >> 5) & 1, w);
     // a box that starts past the piece's rows belongs to the next piece or to nothing
-    if (row0 < q.m_len) st.store(&maps.m[q.out_map], col + c, q.out_off + row0);
-  }
+    if ((c & 32) && row0 < q.m_len) st.store(&maps.m[q.out_map], x - 32, q.out_off + row0);
+  });
 }
 
 // fp32 sums of dH over this piece's (and split's) vocab entries, added to the earlier pieces'.
@@ -450,10 +661,7 @@ __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const Xent
                                                  uint32_t tacc, bool zero, int32_t split,
                                                  int32_t row, bool row_ok, int32_t col) {
   float* dst = p.dh_partial + ((int64_t)split * p.rows_pad + row) * p.H;
-#pragma unroll 1
-  for (int c = 0; c < kXChunk && col + c < p.H; c += 32) {
-    uint32_t r[32];
-    xent_acc32(tacc + (uint32_t)c, zero, r);
+  xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int32_t x = col + c + 4 * j;
@@ -471,7 +679,7 @@ __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const Xent
         *a = v;
       }
     }
-  }
+  });
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -498,10 +706,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const uint32_t done_bar = smem_u32(bars + 2 * S + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // (2 * S is even, so the 16-byte answer slots are aligned)
+  // (2 * S is even, so the 16-byte answer and tile slots are aligned)
   const ClcRing clc{smem_u32(bars + 2 * S + 6), smem_u32(bars + 2 * S + 14),
                     smem_u32(bars + 2 * S + 18)};
-  constexpr uint32_t kReaders = (kPair ? 2u : 1u) * (1u + kXEpiWarps) + 1u;
+  const XentInfo info_ring{smem_u32(bars + 2 * S + 22), smem_u32(bars + 2 * S + 30),
+                           smem_u32(bars + 2 * S + 32)};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -510,7 +719,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
     for (int k = 0; k < kClcSlots; ++k) {
       mbar_init(clc.full0 + 8 * k, 1);
-      mbar_init(clc.empty0 + 8 * k, kReaders);
+      mbar_init(clc.empty0 + 8 * k, kPair ? 2 : 1);  // read by the scheduler warps
+    }
+    for (int k = 0; k < kXInfoSlots; ++k) {
+      mbar_init(info_ring.full0 + 8 * k, 1);
+      // read by the producer, the epilogue warps and, in a pair's leader alone, the MMA warp
+      mbar_init(info_ring.empty0 + 8 * k, 1 + kXEpiWarps + (leader ? 1 : 0));
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -539,7 +753,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
   pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
   const int32_t n_rows = p.n_rows != nullptr ? *p.n_rows : p.rows;
-  const int first_tile = (int)blockIdx.x >> (kPair ? 1 : 0);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -548,73 +761,54 @@ __global__ void __launch_bounds__(kXThreads, 1)
     uint32_t phase = 0;
     int issued = 0;
     bool ok = true;
-    int asked = 0;
-    int tile = first_tile;
-    for (int j = 0; ok && tile >= 0; ++j) {
-      if (leader) {
-        if (!clc_ask<kPair>(clc, j + 1, p.wait, abort_flag)) {
+    for (int j = 0; ok; ++j) {
+      XentTileAt tc;
+      if (!xent_read(info_ring, j, tc, p.wait, abort_flag)) {
+        fail(kRoleProducer, abort_flag);
+        break;
+      }
+      if (tc.prob == -2) break;
+      if (tc.prob < 0) continue;
+      const XentProblem& q = p.prob[tc.prob];
+      const CUtensorMap* ma = &maps.m[q.a_map];
+      const CUtensorMap* mb = &maps.m[q.b_map];
+      // this CTA's part of the tile: 128 rows of A, kBRows of B
+      const int32_t m0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0);
+      const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * T::kBRows : 0) + (q.b_k ? 0 : q.b_off);
+      for (int ks = 0; ks < tc.k_steps; ++ks) {
+        if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, p.wait, abort_flag)) {
           fail(kRoleProducer, abort_flag);
+          ok = false;
           break;
         }
-        asked = j + 1;
-      }
-      const XentTileAt tc = xent_tile<T::kM>(p, n_rows, tile);
-      if (tc.prob >= 0) {
-        const XentProblem& q = p.prob[tc.prob];
-        const CUtensorMap* ma = &maps.m[q.a_map];
-        const CUtensorMap* mb = &maps.m[q.b_map];
-        // this CTA's part of the tile: 128 rows of A, kBRows of B
-        const int32_t m0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0) + q.a_off;
-        const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * T::kBRows : 0) + (q.b_k ? 0 : q.b_off);
-        for (int ks = 0; ks < tc.k_steps; ++ks) {
-          if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, p.wait, abort_flag)) {
-            fail(kRoleProducer, abort_flag);
-            ok = false;
-            break;
-          }
-          if (lane == 0 && !p.wait.starve_loads) {
-            const uint32_t full = full0 + 8 * stage;
-            const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
-            const uint32_t sb = sa + T::kABytes;
-            const int32_t k = (tc.k0 + ks) * kBK;
-            const int32_t kb = k + (q.b_k ? q.b_off : 0);
-            if (leader) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * T::kStageBytes);
+        if (lane == 0 && !p.wait.starve_loads) {
+          const uint32_t full = full0 + 8 * stage;
+          const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
+          const uint32_t sb = sa + T::kABytes;
+          const int32_t k = (tc.k0 + ks) * kBK;
+          const int32_t kb = k + (q.b_k ? q.b_off : 0);
+          if (leader) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * T::kStageBytes);
+          if (q.a_mn)
+            xent_load_3d<kPair>(sa, ma, full, m0, k, pol);
+          else
+            xent_load_2d<kPair>(sa, ma, full, k, m0, pol);
+          if (!q.b_mn) {
+            xent_load_2d<kPair>(sb, mb, full, kb, n0, pol);
+          } else if (!q.b_flat) {
+            xent_load_3d<kPair>(sb, mb, full, n0, kb, pol);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int32_t mn = m0 + 64 * i;
-              const int32_t x = q.a_mn ? mn : k, y = q.a_mn ? k : mn;
-              if constexpr (kPair)
-                tma_load_2d_pair(sa + i * kXBox, ma, full, tma_x((int64_t)x * 2, 2), y, pol);
-              else
-                tma_load_2d(sa + i * kXBox, ma, full, tma_x((int64_t)x * 2, 2), y, pol);
-            }
-#pragma unroll
-            for (int i = 0; i < T::kBRows / 64; ++i) {
-              const int32_t mn = n0 + 64 * i;
-              const int32_t x = q.b_mn ? mn : kb, y = q.b_mn ? kb : mn;
-              if constexpr (kPair)
-                tma_load_2d_pair(sb + i * kXBox, mb, full, tma_x((int64_t)x * 2, 2), y, pol);
-              else
-                tma_load_2d(sb + i * kXBox, mb, full, tma_x((int64_t)x * 2, 2), y, pol);
-            }
-          }
-          __syncwarp();
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+            for (int i = 0; i < T::kBRows / 64; ++i)
+              xent_load_2d<kPair>(sb + i * kXBlock, mb, full, n0 + 64 * i, kb, pol);
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) break;
-      tile = clc_take<kPair>(clc, j + 1, p.wait, abort_flag, ok);
-      if (!ok) fail(kRoleProducer, abort_flag);
-    }
-    // An answer asked for but not read (an error path) must still land before the CTA exits.
-    if (leader && asked > 0) {
-      const int slot = (asked - 1) % kClcSlots;
-      const uint32_t ph = (uint32_t)((asked - 1) / kClcSlots) & 1u;
-      if (!wait_bounded(clc.full0 + 8 * slot, ph, p.wait, nullptr)) fail(kRoleDrain, abort_flag);
     }
     // Drain, as in the fp32 head: loads land (or, for a pair, the stages they filled are
     // released) before the CTA may exit.
@@ -638,63 +832,56 @@ __global__ void __launch_bounds__(kXThreads, 1)
     uint32_t phase = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    bool ok = true;
-    int tile = leader ? first_tile : -1;
-    for (int tj = 0; ok && tile >= 0; ++tj) {
-      const XentTileAt tc = xent_tile<T::kM>(p, n_rows, tile);
-      if (tc.prob >= 0) {
-        const XentProblem& q = p.prob[tc.prob];
-        const uint32_t idesc = idesc0 | ((uint32_t)q.a_mn << 15) | ((uint32_t)q.b_mn << 16);
-        // one K = 16 step further along: 32 bytes in a K-major tile, 16 rows in an MN-major one
-        const uint64_t a_step = q.a_mn ? (16 * 128) >> 4 : 32 >> 4;
-        const uint64_t b_step = q.b_mn ? (16 * 128) >> 4 : 32 >> 4;
-        if (!wait_bounded(tempty0 + 8 * acc, acc_phase ^ 1u, p.wait, abort_flag)) {
+    bool ok = leader;
+    for (int j = 0; ok; ++j) {
+      XentTileAt tc;
+      if (!xent_read(info_ring, j, tc, p.wait, abort_flag)) {
+        fail(kRoleMma, abort_flag);
+        break;
+      }
+      if (tc.prob == -2) break;
+      if (tc.prob < 0) continue;
+      const XentProblem& q = p.prob[tc.prob];
+      const uint32_t idesc = idesc0 | ((uint32_t)q.a_mn << 15) | ((uint32_t)q.b_mn << 16);
+      // one K = 16 step further along: 32 bytes in a K-major tile, 16 rows in an MN-major one
+      const uint64_t a_step = q.a_mn ? (16 * 128) >> 4 : 32 >> 4;
+      const uint64_t b_step = q.b_mn ? (16 * 128) >> 4 : 32 >> 4;
+      if (!wait_bounded(tempty0 + 8 * acc, acc_phase ^ 1u, p.wait, abort_flag)) {
+        fail(kRoleMma, abort_flag);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kXN);
+      for (int ks = 0; ks < tc.k_steps; ++ks) {
+        if (!wait_bounded(full0 + 8 * stage, phase, p.wait, abort_flag)) {
           fail(kRoleMma, abort_flag);
+          ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kXN);
-        for (int ks = 0; ks < tc.k_steps; ++ks) {
-          if (!wait_bounded(full0 + 8 * stage, phase, p.wait, abort_flag)) {
-            fail(kRoleMma, abort_flag);
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
-          const uint32_t sb = sa + T::kABytes;
-          uint64_t ad = q.a_mn ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
-          uint64_t bd = q.b_mn ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
-#pragma unroll
-          for (int i = 0; i < kBK / kUK; ++i) {
-            if constexpr (kPair)
-              mma_bf16_ss_pair_elect(d_tmem, ad, bd, idesc, (ks | i) != 0);
-            else
-              mma_bf16_ss_elect(d_tmem, ad, bd, idesc, (ks | i) != 0);
-            ad += a_step;
-            bd += b_step;
-          }
-          if constexpr (kPair)
-            mma_commit_pair_elect(empty0 + 8 * stage, 0x3);
-          else
-            mma_commit_elect(empty0 + 8 * stage);
-          __syncwarp();
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
+        const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
+        const uint32_t sb = sa + T::kABytes;
+        const uint64_t ad = q.a_mn ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
+        const uint64_t bd = q.b_mn ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
+        mma4_f16_steps_elect<kPair>(d_tmem, ad, bd, a_step, b_step, idesc, ks != 0);
         if constexpr (kPair)
-          mma_commit_pair_elect(tfull0 + 8 * acc, 0x3);
+          mma_commit_pair_elect(empty0 + 8 * stage, 0x3);
         else
-          mma_commit_elect(tfull0 + 8 * acc);
+          mma_commit_elect(empty0 + 8 * stage);
         __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      tile = clc_take<kPair>(clc, tj + 1, p.wait, abort_flag, ok);
-      if (!ok) fail(kRoleMma, abort_flag);
+      if (!ok) break;
+      if constexpr (kPair)
+        mma_commit_pair_elect(tfull0 + 8 * acc, 0x3);
+      else
+        mma_commit_elect(tfull0 + 8 * acc);
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
     if (leader) {
       if constexpr (kPair)
@@ -704,6 +891,38 @@ __global__ void __launch_bounds__(kXThreads, 1)
       __syncwarp();
       if (!wait_bounded(done_bar, 0, p.wait, nullptr)) fail(kRoleDrain, abort_flag);
     }
+  } else if (warp == 2 + kXEpiWarps) {
+    // ---------------------------------------------------------------- scheduler
+    const XentWalk<T::kM> walk(p, n_rows);
+    int tile = (int)blockIdx.x >> (kPair ? 1 : 0);
+    bool ok = true;
+    int asked = 0;
+    for (int j = 0;; ++j) {
+      // the next tile is asked for before this one is announced
+      if (leader && tile >= 0) {
+        if (!clc_ask<kPair>(clc, j + 1, p.wait, abort_flag)) {
+          fail(kRoleProducer, abort_flag);
+          break;
+        }
+        asked = j + 1;
+      }
+      if (!xent_announce(info_ring, j, walk.at(p, tile), tile < 0, p.wait, abort_flag)) {
+        fail(kRoleProducer, abort_flag);
+        break;
+      }
+      if (tile < 0) break;
+      tile = clc_take<kPair>(clc, j + 1, p.wait, abort_flag, ok);
+      if (!ok) {
+        fail(kRoleProducer, abort_flag);
+        break;
+      }
+    }
+    // An answer asked for but not read (an error path) must still land before the CTA exits.
+    if (leader && asked > 0) {
+      const int slot = (asked - 1) % kClcSlots;
+      const uint32_t ph = (uint32_t)((asked - 1) / kClcSlots) & 1u;
+      if (!wait_bounded(clc.full0 + 8 * slot, ph, p.wait, nullptr)) fail(kRoleDrain, abort_flag);
+    }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;      // TMEM lanes this warp may access
@@ -711,41 +930,46 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const XentStage st{smem_u32(staging + (warp - 2) * kXStoreBox)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    bool ok = true;
-    int tile = first_tile;
-    for (int tj = 0; ok && tile >= 0; ++tj) {
-      const XentTileAt tc = xent_tile<T::kM>(p, n_rows, tile);
-      if (tc.prob >= 0) {
-        const XentProblem& q = p.prob[tc.prob];
-        if (!wait_bounded(tfull0 + 8 * acc, acc_phase, p.wait, abort_flag, kSleepHintNs)) {
-          fail(kRoleEpilogue, abort_flag);
-          break;
-        }
-        tc_fence_after_sync();
-        const int32_t row0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0) + quarter * 32;
-        const int32_t row = row0 + lane;
-        const int32_t col = tc.n0 + half * kXChunk;
-        const bool zero = tc.k_steps == 0;
-        const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                              (uint32_t)(acc * kXN + half * kXChunk);
-        if (q.kind == kXentStats)
-          xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, col);
-        else if (q.kind == kXentDlogits)
-          xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, row < n_rows, col);
-        else if (q.kind == kXentDweight)
-          xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, row0, row, col);
-        else
-          xent_epi_dhidden(p, q, tacc, zero, tc.split, row, row < n_rows, col);
-        tc_fence_before_sync();
-        if constexpr (kPair)
-          mbar_arrive_remote(tempty0 + 8 * acc, 0);
-        else
-          mbar_arrive(tempty0 + 8 * acc);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+    for (int j = 0;; ++j) {
+      XentTileAt tc;
+      if (!xent_read(info_ring, j, tc, p.wait, abort_flag, kSleepHintNs)) {
+        fail(kRoleEpilogue, abort_flag);
+        break;
       }
-      tile = clc_take<kPair>(clc, tj + 1, p.wait, abort_flag, ok);
-      if (!ok) fail(kRoleEpilogue, abort_flag);
+      if (tc.prob == -2) break;
+      if (tc.prob < 0) continue;
+      const XentProblem& q = p.prob[tc.prob];
+      const int32_t row0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0) + quarter * 32;
+      const int32_t row = row0 + lane;
+      // what the row needs besides the sums, on its way during the wait
+      int32_t target = -1;
+      float4 info = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+      if (q.kind == kXentStats && row < n_rows) target = p.targets[row];
+      if (q.kind == kXentDlogits && row < n_rows) info = p.row_info[row];
+      if (!wait_bounded(tfull0 + 8 * acc, acc_phase, p.wait, abort_flag, kSleepHintNs)) {
+        fail(kRoleEpilogue, abort_flag);
+        break;
+      }
+      tc_fence_after_sync();
+      const int32_t col = tc.n0 + half * kXChunk;
+      const bool zero = tc.k_steps == 0;
+      const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                            (uint32_t)(acc * kXN + half * kXChunk);
+      if (q.kind == kXentStats)
+        xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
+      else if (q.kind == kXentDlogits)
+        xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row < n_rows, info, col);
+      else if (q.kind == kXentDweight)
+        xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, row0, row, col);
+      else
+        xent_epi_dhidden(p, q, tacc, zero, tc.split, row, row < n_rows, col);
+      tc_fence_before_sync();
+      if constexpr (kPair)
+        mbar_arrive_remote(tempty0 + 8 * acc, 0);
+      else
+        mbar_arrive(tempty0 + 8 * acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_all();  // the stores have left this CTA's shared memory and landed
     __syncwarp();
@@ -832,31 +1056,68 @@ __global__ void __launch_bounds__(kPackThreads)
       packed[(int64_t)r * row_vecs + x] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// ------------------------------------------------------------------ the target's logit
+
+// z of one row's target, summed here in fp32 and not taken from the tensor cores: their fp32
+// accumulator drops low bits at each of its H / 16 steps and comes out about 1e-6 of z low at
+// H = 1024 (twice that at 2048), always towards zero, so the error would not average out over the
+// rows of a mean. The loss is a difference against this one logit; for the others the same loss is
+// a factor of 1 + 1e-6 z in the softmax. Called by a whole warp, the result in every lane.
+template <bool kF16>
+__device__ __forceinline__ float xent_target_logit(const uint4* __restrict__ h,
+                                                   const uint4* __restrict__ w, int32_t row_vecs,
+                                                   const uint16_t* bias, int32_t t, float alpha) {
+  float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 4
+  for (int32_t x = (int)(threadIdx.x & 31); x < row_vecs; x += 32) {
+    const uint4 a = __ldg(h + x), b = __ldg(w + x);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s0 = fmaf(unpack16<kF16>(u[i] & 0xffffu), unpack16<kF16>(v[i] & 0xffffu), s0);
+      s1 = fmaf(unpack16<kF16>(u[i] >> 16), unpack16<kF16>(v[i] >> 16), s1);
+    }
+  }
+  float s = s0 + s1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return alpha * (bias != nullptr ? s + unpack16<kF16>(bias[t]) : s);
+}
+
 // ------------------------------------------------------------------ the loss from the statistics
 
 // Folds each row's (max, sum) pairs in a fixed order (32 segments of consecutive pairs, then the
-// segments) into lse and the row's loss. A block of 32 warps serves 32 rows, lane i row i, so the
-// reads of the pair arrays are 256 bytes wide. Ignored rows get 0 and 0; a target outside [0, V)
-// makes the row's loss NaN.
+// segments), joins the target's term and writes lse and the row's loss. A block of 32 warps serves
+// 32 rows, lane i row i, so the reads of the pair arrays are 256 bytes wide; warp i sums row i's
+// target logit. With x = z * log2(e) and the others' (m, s):
+//   lse - z_t = log1p(s * 2^(m - x_t))                        where the target leads,
+//             = (m - x_t + log2(s + 2^(x_t - m))) / log2(e)   elsewhere,
+// so the loss of a row that is almost sure of its target keeps its bits. Ignored rows get 0 and 0;
+// a target outside [0, V) makes the row's loss NaN, and its lse is that of all entries.
 __device__ __forceinline__ void xent_merge(float& m, float& s, float m2, float s2) {
-  // NaN sums (a NaN or +inf logit) survive both branches: exp of a NaN difference is NaN
+  // NaN sums (a NaN or +inf logit) survive: exp of a NaN difference is NaN, and so is NaN * 0
   const float nm = fmaxf(m, m2);
   const float ref = nm == -INFINITY ? 0.0f : nm;
-  s = s * __expf(m - ref) + s2 * __expf(m2 - ref);
+  s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
   m = nm;
 }
 constexpr int kFoldRows = 32;
+template <bool kF16>
 __global__ void __launch_bounds__(1024)
     xent_fold_kernel(const float2* __restrict__ partials, int32_t n_chunks, int32_t pitch,
                      int32_t rows, int32_t V, const int32_t* __restrict__ place,
-                     const int32_t* __restrict__ targets, const float* __restrict__ target_z,
-                     float z_loss, float* row_loss, float* lse_out) {
+                     const int32_t* __restrict__ targets, const uint4* __restrict__ hidden,
+                     const uint4* __restrict__ W, int32_t row_vecs,
+                     const uint16_t* __restrict__ bias, float alpha, float z_loss,
+                     float* row_loss, float* lse_out) {
   __shared__ float2 seg[32][kFoldRows + 1];
+  __shared__ float s_zt[kFoldRows];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t r = (int32_t)blockIdx.x * kFoldRows + lane;
   const int32_t at = r >= rows ? -1 : place != nullptr ? place[r] : r;
+  const int32_t t = at >= 0 ? targets[r] : -1;
   const int per_seg = (n_chunks + 31) / 32;
   const int c0 = warp * per_seg, c1 = min(n_chunks, c0 + per_seg);
   float m = -INFINITY, s = 0.0f;
@@ -875,6 +1136,15 @@ __global__ void __launch_bounds__(1024)
     }
   }
   seg[warp][lane] = make_float2(m, s);
+  __syncwarp();
+  const int32_t my_r = (int32_t)blockIdx.x * kFoldRows + warp;
+  const int32_t my_t = __shfl_sync(0xffffffffu, t, warp);
+  if (my_t >= 0 && my_t < V) {  // the whole warp
+    const float z = xent_target_logit<kF16>(hidden + (int64_t)my_r * row_vecs,
+                                            W + (int64_t)my_t * row_vecs, row_vecs, bias, my_t,
+                                            alpha);
+    if (lane == 0) s_zt[warp] = z;
+  }
   __syncthreads();
   if (warp != 0 || r >= rows) return;
   if (at < 0) {
@@ -885,9 +1155,21 @@ __global__ void __launch_bounds__(1024)
   m = -INFINITY;
   s = 0.0f;
   for (int w = 0; w < 32; ++w) xent_merge(m, s, seg[w][lane].x, seg[w][lane].y);
-  const float lse = m + logf(s);
-  const int32_t t = targets[at];
-  const float nll = t >= 0 && t < V ? lse - target_z[at] : __int_as_float(0x7fc00000);
+  float lse, nll;
+  if (t >= 0 && t < V) {
+    const float zt = s_zt[lane], xt = zt * kLog2e;
+    if (xt >= m) {
+      nll = log1pf(s * exp2f(m - xt));
+      lse = zt + nll;
+    } else {
+      const float l = log2f(s + exp2f(xt - m));
+      nll = (m - xt + l) * kLn2;
+      lse = (m + l) * kLn2;
+    }
+  } else {
+    lse = (m + log2f(s)) * kLn2;
+    nll = __int_as_float(0x7fc00000);
+  }
   lse_out[r] = lse;
   row_loss[r] = z_loss != 0.0f ? nll + z_loss * lse * lse : nll;
 }
@@ -918,49 +1200,72 @@ __global__ void __launch_bounds__(1024)
 
 // ------------------------------------------------------------------ factors of the gradient
 
-// (lse, a, b, target) of every row that counts, and scale[1] = the factor of the gradients (see the
-// top of this file). One block: the power of two needs the largest factor of all rows first, and
-// the rows are a few thousand numbers. A target outside [0, V) makes its row NaN.
+// (lse * log2(e), a, d at the target, target) of every row that counts, and scale[1] = the factor
+// of the gradients (see the top of this file). The target's entry of d, a p - b, is taken from the
+// target's exact logit as b (p - 1) + (a - b) p with p - 1 = expm1(z_t - lse), so that a row
+// almost sure of its target keeps its small gradient. What its rounding to 16 bits takes away goes
+// to lost[i]: it is the largest entry of most rows, and the one rounding error of dH that is the
+// same in all of a row (xent_finish_hidden_kernel puts it back). The power of two needs the largest factor of
+// all rows first: each block finds it by itself (a few KB that sit in L2), then takes rows 32 at a
+// time, a warp a row. A target outside [0, V) makes its row NaN.
+constexpr int kRowsBlock = 32;
+template <bool kF16>
 __global__ void __launch_bounds__(1024)
     xent_rows_kernel(const float* __restrict__ lse, const int32_t* __restrict__ targets,
                      const int32_t* __restrict__ row_of, int32_t rows,
                      const int32_t* __restrict__ n_rows, int32_t V,
+                     const uint4* __restrict__ hidden, const uint4* __restrict__ W,
+                     int32_t row_vecs, const uint16_t* __restrict__ bias,
                      const float* __restrict__ grad, int32_t per_row, int32_t mean, float z_loss,
-                     float alpha, float4* row_info, float* scale) {
+                     float alpha, float4* row_info, float* lost, float* scale) {
   __shared__ float part[32];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t n = n_rows != nullptr ? *n_rows : rows;
-  auto factors = [&](int32_t i, float& l, float& a, float& b) {
-    const int32_t r = row_of != nullptr ? row_of[i] : i;
-    l = lse[r];
-    b = per_row ? grad[r] : 1.0f;
-    a = z_loss != 0.0f ? b * (1.0f + 2.0f * z_loss * l) : b;
-  };
-  float top = 0.0f;
-  for (int32_t i = threadIdx.x; i < n; i += 1024) {
-    float l, a, b;
-    factors(i, l, a, b);
-    if (fabsf(a) < INFINITY) top = fmaxf(top, fabsf(a));  // (false for NaN)
-    if (fabsf(b) < INFINITY) top = fmaxf(top, fabsf(b));
+  float top = 1.0f;
+  if (per_row || z_loss != 0.0f) {
+    top = 0.0f;
+    for (int32_t i = threadIdx.x; i < n; i += 1024) {
+      const int32_t r = row_of != nullptr ? row_of[i] : i;
+      const float b = per_row ? fabsf(grad[r]) : 1.0f;
+      const float a = fabsf(b * (1.0f + 2.0f * z_loss * lse[r]));
+      if (a < INFINITY) top = fmaxf(top, a);  // (false for NaN)
+      if (b < INFINITY) top = fmaxf(top, b);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) part[warp] = top;
+    __syncthreads();
+    top = part[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-  __syncthreads();
-  top = part[threadIdx.x & 31];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const int k = top > 0.0f ? min(100, max(-100, 13 - ilogbf(top))) : 0;
   const float up = ldexpf(1.0f, k), down = ldexpf(1.0f, -k);
-  for (int32_t i = threadIdx.x; i < n; i += 1024) {
-    float l, a, b;
-    factors(i, l, a, b);
-    const int32_t t = targets[i];
-    if (t < 0 || t >= V) a = b = __int_as_float(0x7fc00000);
-    row_info[i] = make_float4(l, a * up, b * up, __int_as_float(t));
+  for (int32_t i = (int32_t)blockIdx.x * kRowsBlock + warp; i < n;
+       i += (int32_t)gridDim.x * kRowsBlock) {
+    const int32_t r = row_of != nullptr ? row_of[i] : i;
+    const int32_t t = targets[r];
+    const float l = lse[r];
+    const float b = (per_row ? grad[r] : 1.0f) * up;
+    float a = z_loss != 0.0f ? b * (1.0f + 2.0f * z_loss * l) : b;
+    float at_target = __int_as_float(0x7fc00000);
+    if (t >= 0 && t < V) {  // the whole warp
+      const float z = xent_target_logit<kF16>(hidden + (int64_t)r * row_vecs,
+                                              W + (int64_t)t * row_vecs, row_vecs, bias, t, alpha);
+      const float e = expm1f(z - l);
+      at_target = b * e;
+      if (z_loss != 0.0f) at_target += b * (2.0f * z_loss * l) * (e + 1.0f);
+    } else {
+      a = at_target;
+    }
+    if (lane == 0) {
+      row_info[i] = make_float4(l * kLog2e, a, at_target, __int_as_float(t));
+      lost[i] = at_target - unpack16<kF16>(pack16<kF16>(at_target, 0.0f) & 0xffffu);
+    }
   }
-  if (threadIdx.x == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     float f = alpha;
     if (!per_row) f *= mean ? *grad / (float)max(n, 1) : *grad;
     scale[0] = up;
@@ -968,29 +1273,32 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dH from its partial sums: the splits in order, times the factor, rounded once; ignored rows 0.
-// A thread takes 8 entries of a row.
+// dH from its partial sums: the splits in order, plus what the target's entry of d lost in its
+// rounding times the target's row of W, times the factor, rounded once; ignored rows 0. A thread
+// takes 8 entries of a row.
 constexpr int kFinishThreads = 256;
 template <bool kF16>
 __global__ void __launch_bounds__(kFinishThreads)
     xent_finish_hidden_kernel(const float* __restrict__ partial, int32_t splits, int64_t split_len,
-                              int32_t rows, int32_t H, const int32_t* __restrict__ place,
+                              int32_t rows, int32_t row_vecs, const int32_t* __restrict__ place,
+                              const int32_t* __restrict__ targets, int32_t V,
+                              const float* __restrict__ lost, const uint4* __restrict__ W,
                               const float* __restrict__ scale, uint4* d_hidden) {
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
   const int64_t i = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x;
-  const int32_t vecs = H / 8;
-  if (i >= (int64_t)rows * vecs) return;
-  const int32_t r = (int32_t)(i / vecs), x = (int32_t)(i - (int64_t)r * vecs) * 8;
+  if (i >= (int64_t)rows * row_vecs) return;
+  const int32_t r = (int32_t)(i / row_vecs), x = (int32_t)(i - (int64_t)r * row_vecs);
   const int32_t at = place != nullptr ? place[r] : r;
   uint4 out = make_uint4(0u, 0u, 0u, 0u);
   if (at >= 0) {
     const float f = scale[1];
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    const float* src = partial + (int64_t)at * H + x;
+    const float4* src = reinterpret_cast<const float4*>(partial) + ((int64_t)at * row_vecs + x) * 2;
+#pragma unroll 4
     for (int32_t k = 0; k < splits; ++k) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(src + k * split_len));
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(src + k * split_len) + 1);
+      const float4 u = __ldcs(src + k * (split_len / 4));
+      const float4 v = __ldcs(src + k * (split_len / 4) + 1);
       s[0] += u.x;
       s[1] += u.y;
       s[2] += u.z;
@@ -999,6 +1307,17 @@ __global__ void __launch_bounds__(kFinishThreads)
       s[5] += v.y;
       s[6] += v.z;
       s[7] += v.w;
+    }
+    const int32_t t = targets[r];
+    if (t >= 0 && t < V) {  // (elsewhere the row is NaN already)
+      const uint4 q = __ldg(W + (int64_t)t * row_vecs + x);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const float e = lost[at];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[2 * j] = fmaf(e, unpack16<kF16>(w[j] & 0xffffu), s[2 * j]);
+        s[2 * j + 1] = fmaf(e, unpack16<kF16>(w[j] >> 16), s[2 * j + 1]);
+      }
     }
     out.x = pack16<kF16>(s[0] * f, s[1] * f);
     out.y = pack16<kF16>(s[2] * f, s[3] * f);
