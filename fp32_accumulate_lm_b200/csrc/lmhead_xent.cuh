@@ -53,7 +53,8 @@ constexpr int kXN = 256;                  // tile columns (MMA N)
 constexpr int kXBlock = 64 * 64 * 2;      // bytes of 64 K rows of 64 entries of M or N
 constexpr int kXEpiWarps = 8;
 constexpr int kXThreads = 64 + 32 * kXEpiWarps + 32;
-constexpr int kXInfoSlots = 2;            // tiles the scheduler warp announces ahead
+constexpr int kXInfoSlots = 2;            // tile slots of the scheduler warp
+constexpr int kXAskAhead = 12;            // K steps before a tile's end at which the next is taken
 constexpr int kXStoreBox = 32 * 64 * 2;   // an epilogue warp's store box: 32 rows of 64 elements
 constexpr int kXMaxProblems = 3;
 constexpr int kXChunk = 128;              // vocab entries per (max, sum) pair of a row
@@ -382,11 +383,12 @@ struct XentWalk {
 };
 
 // The tiles of a CTA as its scheduler warp announces them to the other roles. That warp asks for
-// tiles by cluster launch control, takes the answers and works out the coordinates, a tile ahead:
-// done by the MMA warp itself, between two tiles, this took 1000 clocks a tile in which nothing
-// was issued.
+// tiles by cluster launch control, takes the answers and works out the coordinates: done by the MMA
+// warp itself, between two tiles, this took 1000 clocks a tile in which nothing was issued. It asks
+// when the producer says that it nears the end of its tile and no sooner: a unit that holds tiles
+// it has not begun leaves other units idle at the launch's end.
 struct XentInfo {
-  uint32_t slot0, full0, empty0;
+  uint32_t slot0, full0, empty0, want;
 };
 
 __device__ __forceinline__ bool xent_announce(const XentInfo& f, int j, const XentTileAt& c,
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const ClcRing clc{smem_u32(bars + 2 * S + 6), smem_u32(bars + 2 * S + 14),
                     smem_u32(bars + 2 * S + 18)};
   const XentInfo info_ring{smem_u32(bars + 2 * S + 22), smem_u32(bars + 2 * S + 30),
-                           smem_u32(bars + 2 * S + 32)};
+                           smem_u32(bars + 2 * S + 32), smem_u32(bars + 2 * S + 34)};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -730,6 +732,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       mbar_init(tfull0 + 8 * a, 1);
       mbar_init(tempty0 + 8 * a, (kPair ? 2 : 1) * 32 * kXEpiWarps);
     }
+    mbar_init(info_ring.want, 1);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -768,7 +771,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
         break;
       }
       if (tc.prob == -2) break;
-      if (tc.prob < 0) continue;
+      const int32_t ask_at = tc.prob < 0 ? 0 : max(0, tc.k_steps - kXAskAhead);
+      if (tc.prob < 0 || tc.k_steps == 0) {
+        if (lane == 0) mbar_arrive(info_ring.want);
+        __syncwarp();
+        continue;
+      }
       const XentProblem& q = p.prob[tc.prob];
       const CUtensorMap* ma = &maps.m[q.a_map];
       const CUtensorMap* mb = &maps.m[q.b_map];
@@ -781,6 +789,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
           ok = false;
           break;
         }
+        if (lane == 0 && ks == ask_at) mbar_arrive(info_ring.want);
         if (lane == 0 && !p.wait.starve_loads) {
           const uint32_t full = full0 + 8 * stage;
           const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
@@ -898,19 +907,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
     bool ok = true;
     int asked = 0;
     for (int j = 0;; ++j) {
-      // the next tile is asked for before this one is announced
-      if (leader && tile >= 0) {
-        if (!clc_ask<kPair>(clc, j + 1, p.wait, abort_flag)) {
-          fail(kRoleProducer, abort_flag);
-          break;
-        }
-        asked = j + 1;
-      }
       if (!xent_announce(info_ring, j, walk.at(p, tile), tile < 0, p.wait, abort_flag)) {
         fail(kRoleProducer, abort_flag);
         break;
       }
       if (tile < 0) break;
+      if (leader) {
+        if (!wait_bounded(info_ring.want, (uint32_t)j & 1u, p.wait, abort_flag, kSleepHintNs) ||
+            !clc_ask<kPair>(clc, j + 1, p.wait, abort_flag)) {
+          fail(kRoleProducer, abort_flag);
+          break;
+        }
+        asked = j + 1;
+      }
       tile = clc_take<kPair>(clc, j + 1, p.wait, abort_flag, ok);
       if (!ok) {
         fail(kRoleProducer, abort_flag);
