@@ -764,21 +764,45 @@ def _ignore(ignore_index) -> int:
     return IGNORE_NONE if ignore_index is None else int(ignore_index)
 
 
+class _Here:
+    """The launch target where device and stream are torch's current ones already."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle: int):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device and the call's stream as torch's current ones: the kernels launch on
-    this device, and memory allocated for the call belongs to the stream that uses it."""
+def _there(device, stream):
     import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _on(device, stream):
+    """Context of a call: the tensors' device and the call's stream become torch's current ones, so
+    the kernels launch on that device and memory allocated for the call belongs to the stream that
+    uses it. Gives the stream's handle."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        # (torch.cuda.current_stream() builds a Stream object for it, a few microseconds)
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
             torch.cuda.default_stream(device)
-    _check(stream is None or stream.device == device, f"the stream must be one of {device}")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream must be one of {device}")
+    return _there(device, stream)
 
 
 def _workspace(workspace, need: int, device):
@@ -798,29 +822,40 @@ def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+def _dtype_code(t, what: str) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype is torch.float16:
+        return DTYPE_F16
+    raise ValueError(f"{what} must be bf16 or fp16")
+
+
 def _check_head(hidden, W, targets, bias):
     """The inputs of the cross entropy; returns (dtype code, rows, H, V)."""
     import torch
-    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(hidden.dtype)
-    _check(dt is not None and W.dtype == hidden.dtype, "bf16 or fp16 operands of one dtype required")
+    dt = _dtype_code(hidden, "hidden")
+    dev = hidden.device
+    _check(W.dtype is hidden.dtype, "bf16 or fp16 operands of one dtype required")
     _check(hidden.dim() == 2 and W.dim() == 2 and hidden.shape[1] == W.shape[1], "shape mismatch")
     _check(hidden.is_cuda and W.is_cuda and hidden.is_contiguous() and W.is_contiguous(),
            "contiguous CUDA tensors required")
     rows, H = hidden.shape
     V = W.shape[0]
-    _check(W.device == hidden.device, "hidden and W must be on one device")
-    _check(targets.dtype == torch.int32 and targets.is_cuda and targets.is_contiguous()
-           and tuple(targets.shape) == (rows,), "targets must be a contiguous int32 [rows] tensor")
-    _check(targets.device == hidden.device, "targets must be on the inputs' device")
+    _check(W.device == dev, "hidden and W must be on one device")
+    _check(targets.dtype is torch.int32 and targets.is_cuda and targets.is_contiguous()
+           and targets.shape == (rows,), "targets must be a contiguous int32 [rows] tensor")
+    _check(targets.device == dev, "targets must be on the inputs' device")
     if bias is not None:
-        _check(bias.dtype == hidden.dtype and bias.is_cuda and bias.is_contiguous()
-               and tuple(bias.shape) == (V,), "bias must be a contiguous [V] tensor of the dtype")
-        _check(bias.device == hidden.device, "bias must be on the inputs' device")
+        _check(bias.dtype is hidden.dtype and bias.is_cuda and bias.is_contiguous()
+               and bias.shape == (V,), "bias must be a contiguous [V] tensor of the dtype")
+        _check(bias.device == dev, "bias must be on the inputs' device")
     return dt, rows, H, V
 
 
 def _reduction(reduction: str) -> int:
-    _check(reduction in REDUCTIONS, f"reduction must be one of {sorted(REDUCTIONS)}")
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
     return REDUCTIONS[reduction]
 
 
@@ -851,7 +886,7 @@ def cross_entropy_f32(hidden, W, targets, alpha: float = 1.0, bias=None, ignore_
         st = lmhead_cross_entropy_f32(hidden.data_ptr(), dt, rows, H, W.data_ptr(), V, float(alpha),
                                       _ptr(bias), targets.data_ptr(), _ignore(ignore_index),
                                       float(z_loss), red, loss.data_ptr(), lse.data_ptr(),
-                                      ws.data_ptr(), _nbytes(ws), s.cuda_stream)
+                                      ws.data_ptr(), _nbytes(ws), s)
         _finish(st, "lmhead_cross_entropy_f32", check, s)
     return loss, lse
 
@@ -896,16 +931,14 @@ def cross_entropy_grad(hidden, W, targets, lse, grad_loss, alpha: float = 1.0, b
                                        _ignore(ignore_index), float(z_loss), red, lse.data_ptr(),
                                        grad_loss.data_ptr(), _ptr(out[0]), _ptr(out[1]),
                                        _ptr(out[2]), 1 if accumulate else 0, ws.data_ptr(),
-                                       _nbytes(ws), s.cuda_stream)
+                                       _nbytes(ws), s)
         _finish(st, "lmhead_cross_entropy_grad", check, s)
     return tuple(out)
 
 
-def _check_table(t, what: str):
-    import torch
-    dt = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(t.dtype)
-    _check(dt is not None, f"{what} must be bf16 or fp16")
-    _check(t.is_cuda and t.is_contiguous(), f"{what} must be a contiguous CUDA tensor")
+def _check_table(t, what: str) -> int:
+    dt = _dtype_code(t, what)
+    _check(t.is_cuda and t.is_contiguous(), "contiguous CUDA tensors required")
     return dt
 
 
@@ -933,7 +966,7 @@ def embedding(ids, W, scale: float = 1.0, v_begin: int = 0, out=None, stream=Non
         if out is None:
             out = torch.empty(shape, dtype=W.dtype, device=W.device)
         st = lmhead_embedding(ids.data_ptr(), ids.numel(), W.data_ptr(), dt, V, int(v_begin), H,
-                              float(scale), out.data_ptr(), s.cuda_stream)
+                              float(scale), out.data_ptr(), s)
         _finish(st, "lmhead_embedding", check, s)
     return out
 
@@ -963,6 +996,6 @@ def embedding_grad(d_out, ids, V: int, scale: float = 1.0, v_begin: int = 0,
         ws = _workspace(workspace, embedding_grad_workspace_bytes(tokens, V, H), dev)
         st = lmhead_embedding_grad(d_out.data_ptr(), dt, ids.data_ptr(), tokens, V, int(v_begin), H,
                                    float(scale), out.data_ptr(), 1 if accumulate else 0,
-                                   ws.data_ptr(), _nbytes(ws), s.cuda_stream)
+                                   ws.data_ptr(), _nbytes(ws), s)
         _finish(st, "lmhead_embedding_grad", check, s)
     return out

@@ -114,17 +114,22 @@ struct XentBackward {
   XentPack pack;
   float4* row_info;
   float *lost, *scale;
+  int32_t* first;
+  float *side, *side_bias;
   uint16_t* d[2];
   float* dh_partial;
 };
 
-XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_t H,
+XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_t H, int64_t V,
                             bool ignoring) {
   XentBackward b;
   b.pack = carve_pack(c, rows, H, ignoring);
   b.row_info = c.take<float4>(rows);
   b.lost = c.take<float>(rows);
   b.scale = c.take<float>(2);
+  b.first = c.take<int32_t>(V);
+  b.side = c.take<float>(rows * H);
+  b.side_bias = c.take<float>(rows);
   b.d[0] = c.take<uint16_t>(x.rows_pad * x.piece);
   b.d[1] = x.n_pieces > 1 ? c.take<uint16_t>(x.rows_pad * x.piece) : b.d[0];
   b.dh_partial = c.take<float>((int64_t)x.splits * x.rows_pad * H);
@@ -147,9 +152,12 @@ int check_xent_args(const void* hidden, int dtype, int64_t rows, int64_t H, cons
 
 int launch_pack(const XentPack& k, const void* hidden, const int32_t* targets, int64_t rows,
                 int64_t H, int64_t ignore_index, lmhead_stream_t stream) {
-  const unsigned blocks = (unsigned)((rows + lmh::kPackRows - 1) / lmh::kPackRows);
+  // a row a warp, so that few rows are copied by many blocks; for many rows 32 a block, since each
+  // block reads all targets
+  const int32_t block_rows = rows <= 8192 ? lmh::kPackThreads / 32 : lmh::kPackRows;
+  const unsigned blocks = (unsigned)((rows + block_rows - 1) / block_rows);
   return launch_head(lmh::xent_pack_kernel, blocks, lmh::kPackThreads, 0, stream, 1u,
-                     reinterpret_cast<const uint4*>(hidden), targets, (int32_t)rows,
+                     reinterpret_cast<const uint4*>(hidden), targets, (int32_t)rows, block_rows,
                      (int32_t)(H / 8), (int32_t)ignore_index, k.hidden, k.targets, k.place,
                      k.row_of, k.n_rows);
 }
@@ -259,17 +267,19 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
   if (st != LMHEAD_OK) return st;
 
-  float* row_loss = reduction == LMHEAD_REDUCE_NONE ? loss : f.row_loss;
+  const bool each = reduction == LMHEAD_REDUCE_NONE, mean = reduction == LMHEAD_REDUCE_MEAN;
+  const bool one_block = rows <= lmh::kFoldRows;
+  float* row_loss = each ? loss : f.row_loss;
   st = launch_head(fp16 ? lmh::xent_fold_kernel<true> : lmh::xent_fold_kernel<false>,
                    (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows), 1024, 0, stream, 1u,
                    (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
                    (int32_t)rows, (int32_t)V, (const int32_t*)k.place, targets,
                    reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
-                   (int32_t)(H / 8), p.bias, alpha, z_loss, row_loss, lse);
-  if (st != LMHEAD_OK || reduction == LMHEAD_REDUCE_NONE) return st;
+                   (int32_t)(H / 8), p.bias, alpha, z_loss, row_loss, lse,
+                   (const int32_t*)k.n_rows, (int32_t)mean, !each && one_block ? loss : nullptr);
+  if (st != LMHEAD_OK || each || one_block) return st;
   return launch_head(lmh::xent_reduce_kernel, 1, 1024, 0, stream, 1u, (const float*)row_loss,
-                     (int32_t)rows, (const int32_t*)k.n_rows,
-                     (int32_t)(reduction == LMHEAD_REDUCE_MEAN), loss);
+                     (int32_t)rows, (const int32_t*)k.n_rows, (int32_t)mean, loss);
 }
 
 int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, const void* W,
@@ -289,7 +299,9 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
     if (st != LMHEAD_OK) return st;
   }
+  // 32 rows a block, and 4096 entries of the table that it clears
   int64_t row_blocks = (rows + lmh::kRowsBlock - 1) / lmh::kRowsBlock;
+  if (row_blocks < (V + 4095) / 4096) row_blocks = (V + 4095) / 4096;
   if (row_blocks > 2 * dev.num_sms) row_blocks = 2 * dev.num_sms;
   st = launch_head(fp16 ? lmh::xent_rows_kernel<true> : lmh::xent_rows_kernel<false>,
                    (unsigned)row_blocks, 1024, 0, stream, 1u, lse, targets,
@@ -297,7 +309,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
                    reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
                    (int32_t)(H / 8), reinterpret_cast<const uint16_t*>(bias), grad_loss,
                    (int32_t)(reduction == LMHEAD_REDUCE_NONE),
-                   (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.lost, b.scale);
+                   (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.lost, b.scale, b.first);
   if (st != LMHEAD_OK) return st;
 
   // the forms of hidden and W as B's MN-major operand: in 3-D boxes, or where H is no multiple of
@@ -333,6 +345,9 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   p.group = 16;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
+  p.targets = ignoring ? k.targets : targets;
+  p.first = b.first;
+  p.side = b.side;
   p.row_info = b.row_info;
   p.scale = b.scale;
   p.d_weight = reinterpret_cast<uint16_t*>(d_W);
@@ -358,7 +373,8 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
       st = launch_head(fp16 ? lmh::xent_bias_kernel<true> : lmh::xent_bias_kernel<false>, blocks,
                        256, 0, stream, 1u, (const uint16_t*)b.d[c & 1], (int32_t)x.piece,
                        (int32_t)length(c), (int32_t)rows, (const int32_t*)k.n_rows,
-                       (const float*)b.scale, (int32_t)(accumulate != 0),
+                       (const float*)b.scale, (const int32_t*)(b.first + start(c)), b.side_bias,
+                       (int32_t)(accumulate != 0),
                        reinterpret_cast<uint16_t*>(d_bias) + start(c));
       if (st != LMHEAD_OK) return st;
     }
@@ -390,15 +406,39 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     if (c + 1 < x.n_pieces) p.prob[p.n_problems++] = logits_of(c + 1);
     if (p.n_problems > 0) st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
   }
-  if (st != LMHEAD_OK || d_hidden == nullptr) return st;
-  const int64_t vecs = rows * (H / 8);
-  return launch_head(
-      fp16 ? lmh::xent_finish_hidden_kernel<true> : lmh::xent_finish_hidden_kernel<false>,
-      (unsigned)((vecs + lmh::kFinishThreads - 1) / lmh::kFinishThreads), lmh::kFinishThreads, 0,
-      stream, 1u, (const float*)b.dh_partial, x.splits, x.rows_pad * H, (int32_t)rows,
-      (int32_t)(H / 8), (const int32_t*)k.place, targets, (int32_t)V, (const float*)b.lost,
-      reinterpret_cast<const uint4*>(W), (const float*)b.scale,
-      reinterpret_cast<uint4*>(d_hidden));
+  if (st != LMHEAD_OK) return st;
+  lmh::XentFinishParams f = {};
+  f.rows = (int32_t)rows;
+  f.H = (int32_t)H;
+  f.V = (int32_t)V;
+  f.n_rows = k.n_rows;
+  f.place = k.place;
+  f.targets = targets;
+  f.packed_targets = p.targets;
+  f.lost = b.lost;
+  f.scale = b.scale;
+  f.splits = x.splits;
+  f.split_len = x.rows_pad * H;
+  f.partial = b.dh_partial;
+  f.W = reinterpret_cast<const uint4*>(W);
+  f.d_hidden = reinterpret_cast<uint4*>(d_hidden);
+  f.first = b.first;
+  f.side = b.side;
+  f.side_bias = b.side_bias;
+  f.hidden = reinterpret_cast<const uint4*>(h);
+  f.d_weight = reinterpret_cast<uint4*>(d_W);
+  f.d_bias = reinterpret_cast<uint16_t*>(d_bias);
+  const int64_t hidden_blocks =
+      d_hidden == nullptr ? 0 : (rows * (H / 8) + lmh::kFinishThreads - 1) / lmh::kFinishThreads;
+  const int64_t slices =
+      d_W == nullptr ? 1 : (H / 8 + lmh::kFinishThreads - 1) / lmh::kFinishThreads;
+  const int64_t weight_blocks = d_W == nullptr && d_bias == nullptr ? 0 : rows * slices;
+  if (hidden_blocks + weight_blocks > kInt32Max) return LMHEAD_ERR_SHAPE;
+  f.hidden_blocks = (int32_t)hidden_blocks;
+  f.slices = (int32_t)slices;
+  return launch_head(fp16 ? lmh::xent_finish_kernel<true> : lmh::xent_finish_kernel<false>,
+                     (unsigned)(hidden_blocks + weight_blocks), lmh::kFinishThreads, 0, stream, 1u,
+                     f);
 }
 
 int cleared(int st) {
@@ -426,33 +466,38 @@ struct EmbedPlan {
 };
 
 // Digits of equal width, as few passes as 9 bits a digit allow, that hold every id and the mark V.
-// The sums' tile is 64 entries, and longer for many tokens, so that a run through all of them
-// is joined from at most 256 parts (or tiles of 1024); at 16384 tokens 64 entries still give 256
-// blocks a column slice.
-EmbedPlan embed_plan(int64_t tokens, int64_t V) {
+// The sums take at least 8 entries a block, and as many as leave 4096 blocks (two waves; 16384
+// tokens of 4096 columns: the sums 197 us in tiles of 16 and of 64, but the join, a block for each
+// tile and slice of columns, 21 us against 9; few tokens still make many blocks: 1025 tokens of 264
+// columns take 15 us in tiles of 64, 5 in tiles of 8) and 1024 tiles, so that a run through all
+// tokens is joined from at most 1024 parts (up to a million tokens: tiles end at 1024 entries).
+EmbedPlan embed_plan(int64_t tokens, int64_t V, int64_t H) {
   EmbedPlan e;
   int bits = 1;
   while (((int64_t)1 << bits) <= V) ++bits;
   e.passes = (bits + lmh::kSortBits - 1) / lmh::kSortBits;
   e.bits = (bits + e.passes - 1) / e.passes;
-  e.tile = 64;
-  while (e.tile < lmh::kSumTileMax && (int64_t)e.tile * 256 < tokens) e.tile *= 2;
+  e.tile = lmh::kSumTileMin;
+  const int64_t slices = (H + lmh::kSumCols - 1) / lmh::kSumCols;
+  const int64_t tiles = slices < 4 ? 1024 : slices < 4096 ? 4096 / slices : 1;
+  while (e.tile < lmh::kSumTileMax && (int64_t)e.tile * tiles < tokens) e.tile *= 2;
   e.tiles = (int32_t)((tokens + e.tile - 1) / e.tile);
   return e;
 }
 
 struct EmbedScratch {
-  int32_t *keys[2], *pos[2], *hist;
+  int32_t *keys[2], *pos[2];
+  uint32_t* seen;
   float* part;
 };
 
-EmbedScratch carve_embed(Carver& c, const EmbedPlan& e, int64_t tokens, int64_t H) {
+EmbedScratch carve_embed(Carver& c, const EmbedPlan& e, int64_t tokens, int64_t V, int64_t H) {
   EmbedScratch s;
   for (int i = 0; i < 2; ++i) {
     s.keys[i] = c.take<int32_t>(tokens);
     s.pos[i] = c.take<int32_t>(tokens);
   }
-  s.hist = c.take<int32_t>((int64_t)e.passes * lmh::kSortCtas * lmh::kSortDigits);
+  s.seen = c.take<uint32_t>((V + 31) / 32);
   s.part = c.take<float>((int64_t)e.tiles * 2 * H);
   return s;
 }
@@ -483,16 +528,21 @@ int run_embed_grad(const DeviceInfo& dev, const void* d_out, int dtype, const in
     q.keys[i] = s.keys[i];
     q.pos[i] = s.pos[i];
   }
-  q.hist = s.hist;
+  // the rows that the sort's launch clears: about what the device writes while the sort runs
+  const int64_t row_bytes = H * 2;
+  int64_t head = accumulate ? 0 : (((int64_t)24 << 20) + 2048 * tokens) / row_bytes;
+  if (head > V) head = V;
+  const int64_t rest = accumulate ? 0 : V - head;
   unsigned clusters = 1;
-  if (!accumulate) {
+  if (head > 0) {
     q.zero = reinterpret_cast<uint4*>(d_W);
-    q.zero_vecs = V * (H / 8);
-    // two CTAs of 1024 threads an SM, or as many as the table has work for
+    q.zero_vecs = head * (H / 8);
+    // two CTAs of 1024 threads an SM, or as many as the rows have work for
     int64_t fill = (q.zero_vecs + 4 * lmh::kSortThreads - 1) / (4 * lmh::kSortThreads);
     if (fill > 2 * dev.num_sms) fill = 2 * dev.num_sms;
     clusters += (unsigned)((fill + lmh::kSortCtas - 1) / lmh::kSortCtas);
   }
+  if (rest > 0) q.seen = s.seen;
   int st = launch_head(lmh::embed_sort_kernel, clusters * lmh::kSortCtas, lmh::kSortThreads, 0,
                        stream, lmh::kSortCtas, q);
   if (st != LMHEAD_OK) return st;
@@ -509,12 +559,20 @@ int run_embed_grad(const DeviceInfo& dev, const void* d_out, int dtype, const in
   p.add = accumulate != 0;
   p.d_weight = reinterpret_cast<uint16_t*>(d_W);
   p.part = s.part;
-  const unsigned slices = (unsigned)((H + lmh::kSumCols - 1) / lmh::kSumCols);
+  p.slices = (int32_t)((H + lmh::kSumCols - 1) / lmh::kSumCols);
+  p.seen = s.seen;
+  p.zero_from = (int32_t)head;
+  p.zero_rows = (int32_t)(lmh::kZeroVecs / (H / 8) > 1 ? lmh::kZeroVecs / (H / 8) : 1);
+  const int64_t sums = (int64_t)e.tiles * p.slices;
+  const int64_t zeros = (rest + p.zero_rows - 1) / p.zero_rows;
+  if (sums + zeros > kInt32Max) return LMHEAD_ERR_SHAPE;
+  p.sum_blocks = (int32_t)sums;
   st = launch_head(fp16 ? lmh::embed_sum_kernel<true> : lmh::embed_sum_kernel<false>,
-                   dim3((unsigned)e.tiles, slices), lmh::kSumThreads, 0, stream, 1u, p);
+                   (unsigned)(sums + zeros), lmh::kSumThreads, 0, stream, 1u, p);
   if (st != LMHEAD_OK || e.tiles == 1) return st;
   return launch_head(fp16 ? lmh::embed_join_kernel<true> : lmh::embed_join_kernel<false>,
-                     dim3((unsigned)(e.tiles - 1), slices), lmh::kSumThreads, 0, stream, 1u, p);
+                     dim3((unsigned)(e.tiles - 1), (unsigned)p.slices),
+                     lmh::kJoinGroups * lmh::kSumThreads, 0, stream, 1u, p);
 }
 
 }  // namespace
@@ -533,7 +591,7 @@ size_t lmhead_cross_entropy_grad_workspace_bytes(int64_t rows, int64_t H, int64_
                                                  int64_t ignore_index) {
   if (!xent_sizes_ok(rows, H, V)) return 0;
   Carver c(nullptr);
-  carve_backward(c, xent_pieces(rows, H, V), rows, H, ignore_index != LMHEAD_IGNORE_NONE);
+  carve_backward(c, xent_pieces(rows, H, V), rows, H, V, ignore_index != LMHEAD_IGNORE_NONE);
   return (size_t)c.used;
 }
 
@@ -613,7 +671,7 @@ int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64
   if (st != LMHEAD_OK) return st;
   const XentPieces x = xent_pieces(rows, H, V);
   Carver c(workspace);
-  const XentBackward b = carve_backward(c, x, rows, H, ignore_index != LMHEAD_IGNORE_NONE);
+  const XentBackward b = carve_backward(c, x, rows, H, V, ignore_index != LMHEAD_IGNORE_NONE);
   return cleared(run_xent_backward(hidden, dtype, rows, H, W, V, alpha, bias, targets, ignore_index,
                                    z_loss, reduction, lse, grad_loss, d_hidden, d_W, d_bias,
                                    accumulate, x, b, stream));
@@ -647,7 +705,7 @@ size_t lmhead_embedding_grad_workspace_bytes(int64_t tokens, int64_t V, int64_t 
   if (tokens <= 0 || V <= 0 || H <= 0 || tokens >= kTrainMax || V >= kTrainMax || H >= kTrainMax)
     return 0;
   Carver c(nullptr);
-  carve_embed(c, embed_plan(tokens, V), tokens, H);
+  carve_embed(c, embed_plan(tokens, V, H), tokens, V, H);
   return (size_t)c.used;
 }
 
@@ -676,9 +734,9 @@ int lmhead_embedding_grad(const void* d_out, int dtype, const int32_t* ids, int6
   if ((H + lmh::kSumCols - 1) / lmh::kSumCols > 65535) return LMHEAD_ERR_SHAPE;  // grid rows
   st = current_device(&dev);
   if (st != LMHEAD_OK) return st;
-  const EmbedPlan e = embed_plan(tokens, V);
+  const EmbedPlan e = embed_plan(tokens, V, H);
   Carver c(workspace);
-  const EmbedScratch s = carve_embed(c, e, tokens, H);
+  const EmbedScratch s = carve_embed(c, e, tokens, V, H);
   return cleared(run_embed_grad(dev, d_out, dtype, ids, tokens, V, v_begin, H, scale, d_W,
                                 accumulate, e, s, stream));
 }
