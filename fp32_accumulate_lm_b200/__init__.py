@@ -40,7 +40,8 @@ __all__ = [
     "REDUCTIONS", "IGNORE_NONE", "lmhead_cross_entropy_f32", "lmhead_cross_entropy_grad",
     "cross_entropy_workspace_bytes", "cross_entropy_grad_workspace_bytes", "cross_entropy_f32",
     "cross_entropy_grad", "lmhead_embedding", "lmhead_embedding_grad",
-    "embedding_grad_workspace_bytes", "embedding", "embedding_grad",
+    "embedding_grad_workspace_bytes", "embedding", "embedding_grad", "linear_cross_entropy",
+    "embed",
 ]
 
 STATUS = {
@@ -999,3 +1000,96 @@ def embedding_grad(d_out, ids, V: int, scale: float = 1.0, v_begin: int = 0,
                                    ws.data_ptr(), _nbytes(ws), s)
         _finish(st, "lmhead_embedding_grad", check, s)
     return out
+
+
+# ---------------------------------------------------------------- autograd
+
+_functions = None
+
+
+def _autograd_functions():
+    """The torch.autograd.Function classes of the two differentiable entries (made on first use:
+    importing this package does not import torch)."""
+    global _functions
+    if _functions is not None:
+        return _functions
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class LinearCrossEntropy(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, hidden, W, bias, targets, how):
+            loss, lse = cross_entropy_f32(hidden, W, targets, bias=bias, **how)
+            ctx.save_for_backward(hidden, W, bias, targets, lse)
+            ctx.how = how
+            return loss
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad):
+            _refuse_capture("linear_cross_entropy's backward")
+            hidden, W, bias, targets, lse = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            out = tuple(torch.empty_like(t) if n else None
+                        for t, n in zip((hidden, W, bias), need))
+            if any(o is not None for o in out):
+                cross_entropy_grad(hidden, W, targets, lse, grad.contiguous(), bias=bias, out=out,
+                                   **ctx.how)
+            return (*out, None, None)
+
+    class Embed(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, W, ids, scale, v_begin):
+            ctx.save_for_backward(ids)
+            ctx.args = (W.shape[0], scale, v_begin)
+            return embedding(ids, W, scale, v_begin)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad):
+            _refuse_capture("embed's backward")
+            (ids,) = ctx.saved_tensors
+            V, scale, v_begin = ctx.args
+            return embedding_grad(grad.contiguous(), ids, V, scale, v_begin), None, None, None
+
+    _functions = LinearCrossEntropy, Embed
+    return _functions
+
+
+def _refuse_capture(what: str):
+    """Autograd during a stream capture: a gradient accumulator that some other, eager graph of the
+    same leaf keeps alive runs on that graph's stream, which ends the process from a thread of the
+    autograd engine. The plain entries can be captured."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what} cannot be captured into a CUDA graph: capture "
+                           "cross_entropy_f32, cross_entropy_grad, embedding and embedding_grad")
+
+
+def linear_cross_entropy(hidden, W, targets, alpha: float = 1.0, bias=None, ignore_index=-100,
+                         z_loss: float = 0.0, reduction: str = "mean"):
+    """cross_entropy_f32's loss as a torch operation: differentiable in ``hidden`` [..., H], ``W`` and
+    ``bias`` by cross_entropy_grad, on torch's current stream. ``targets`` is int32 [...]; "none"
+    gives a loss of that shape. Not differentiable twice, and refused in a CUDA graph capture where
+    a gradient is wanted (cross_entropy_f32 and cross_entropy_grad can be captured)."""
+    import torch
+    _check(hidden.dim() >= 1 and tuple(hidden.shape[:-1]) == tuple(targets.shape),
+           "hidden must be [*targets.shape, H]")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (hidden, W, bias)):
+        _refuse_capture("linear_cross_entropy with a gradient")
+    fn = _autograd_functions()[0]
+    how = {"alpha": float(alpha), "ignore_index": ignore_index, "z_loss": float(z_loss),
+           "reduction": reduction}
+    loss = fn.apply(hidden.reshape(-1, hidden.shape[-1]).contiguous(), W, bias,
+                    targets.reshape(-1), how)
+    return loss.reshape(targets.shape) if reduction == "none" else loss
+
+
+def embed(ids, W, scale: float = 1.0, v_begin: int = 0):
+    """``embedding`` as a torch operation: differentiable in the table ``W`` by embedding_grad, on
+    torch's current stream. Not differentiable twice, and refused in a CUDA graph capture where a
+    gradient is wanted (embedding and embedding_grad can be captured)."""
+    import torch
+    if torch.is_grad_enabled() and W.requires_grad:
+        _refuse_capture("embed with a gradient")
+    return _autograd_functions()[1].apply(W, ids, float(scale), int(v_begin))
