@@ -115,7 +115,7 @@ struct XentBackward {
   float4* row_info;
   float *lost, *scale;
   int32_t* first;
-  float *side, *side_bias;
+  float *side, *side_bias, *bias_part[2];
   uint16_t* d[2];
   float* dh_partial;
 };
@@ -131,6 +131,7 @@ XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_
   b.side = c.take<float>(rows * H);
   b.side_bias = c.take<float>(rows);
   b.d[0] = c.take<uint16_t>(x.rows_pad * x.piece);
+  for (int i = 0; i < 2; ++i) b.bias_part[i] = c.take<float>(x.rows_pad / 32 * x.piece);
   b.d[1] = x.n_pieces > 1 ? c.take<uint16_t>(x.rows_pad * x.piece) : b.d[0];
   b.dh_partial = c.take<float>((int64_t)x.splits * x.rows_pad * H);
   return b;
@@ -364,6 +365,8 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     q.out_map = lmh::kMapDStore + (c & 1);
     return q;
   };
+  p.piece = (int32_t)x.piece;
+  p.bias_part = d_bias != nullptr ? b.bias_part[0] : nullptr;
   p.n_problems = 1;
   p.prob[0] = logits_of(0);
   st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
@@ -371,13 +374,15 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
     if (d_bias != nullptr) {
       const unsigned blocks = (unsigned)((length(c) + lmh::kBiasCols - 1) / lmh::kBiasCols);
       st = launch_head(fp16 ? lmh::xent_bias_kernel<true> : lmh::xent_bias_kernel<false>, blocks,
-                       256, 0, stream, 1u, (const uint16_t*)b.d[c & 1], (int32_t)x.piece,
+                       lmh::kBiasCols * lmh::kBiasParts, 0, stream, 1u,
+                       (const float*)b.bias_part[c & 1], (int32_t)x.piece,
                        (int32_t)length(c), (int32_t)rows, (const int32_t*)k.n_rows,
                        (const float*)b.scale, (const int32_t*)(b.first + start(c)), b.side_bias,
                        (int32_t)(accumulate != 0),
                        reinterpret_cast<uint16_t*>(d_bias) + start(c));
       if (st != LMHEAD_OK) return st;
     }
+    if (d_bias != nullptr) p.bias_part = b.bias_part[(c + 1) & 1];
     p.n_problems = 0;
     if (d_hidden != nullptr) {  // the longest tiles first
       lmh::XentProblem q = xent_problem(lmh::kXentDhidden, lmh::kMapD + (c & 1),

@@ -131,6 +131,8 @@ struct XentParams {
   float2* partials;           // stats: [2 * ceil(V / 256)][rows]
   const float4* row_info;     // dlogits: (lse * log2(e), a, d at the target, target as int bits)
   const float* scale;         // device: [1] = the factor of the gradients
+  float* bias_part;           // dlogits: [rows_pad / 32][piece] column sums of d, or null
+  int32_t piece;              // entries of a full piece (the pitch of bias_part)
   int32_t* first;             // [V]: the first row whose target is this entry (kXNoRow: none)
   float* side;                // [rows that count][H]: dW's row of that target before its rounding
   uint16_t* d_weight;         // dW as memory, for add
@@ -562,6 +564,24 @@ struct XentStage {
       st_shared_v4(buf + row * 128u + (((uint32_t)(half * 4 + j) ^ (row & 7u)) << 4), w[4 * j],
                    w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
+  // The box's columns 2 * lane and 2 * lane + 1 summed over its 32 rows, in order.
+  template <bool kF16>
+  __device__ __forceinline__ float2 column_sums() const {
+    const uint32_t lane = threadIdx.x & 31;
+    __syncwarp();
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+    for (uint32_t row = 0; row < 32; ++row) {
+      uint32_t w;
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w)
+                   : "r"(buf + row * 128u + (((lane >> 2) ^ (row & 7u)) << 4) + (lane & 3u) * 4u)
+                   : "memory");
+      s.x += unpack16<kF16>(w & 0xffffu);
+      s.y += unpack16<kF16>(w >> 16);
+    }
+    return s;
+  }
   __device__ __forceinline__ void store(const CUtensorMap* map, int32_t x, int32_t y) const {
     fence_async_smem();
     __syncwarp();
@@ -588,6 +608,7 @@ __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const Xent
                                                  uint32_t tacc, bool zero, int32_t row0,
                                                  int32_t row, bool row_ok, const float4& info,
                                                  int32_t col) {
+  const int lane = threadIdx.x & 31;
   const int32_t V = q.b_off + q.n_len;  // the end of the piece as vocab ids
   const int32_t t = __float_as_int(info.w);
   const uint64_t a2 = pair_f32(info.y, info.y);
@@ -621,7 +642,14 @@ __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const Xent
     xent_pack32<kF16>(r, w);
     if ((c & 32) == 0) st.begin();
     st.put((c >> 5) & 1, w);
-    if (c & 32) st.store(&maps.m[q.out_map], col + c - 32, row0);
+    if (c & 32) {
+      const int32_t x = col + c - 32;
+      if (p.bias_part != nullptr) {
+        const float2 sums = st.column_sums<kF16>();
+        reinterpret_cast<float2*>(p.bias_part + (int64_t)(row0 / 32) * p.piece + x)[lane] = sums;
+      }
+      st.store(&maps.m[q.out_map], x, row0);
+    }
   });
 }
 
@@ -1478,48 +1506,39 @@ __global__ void __launch_bounds__(kFinishThreads)
     xent_finish_weight<kF16>(p);
 }
 
-// dbias of a piece: the columns of d summed over the rows that count, in fp32. A block takes 64
-// columns: 8 threads of 8 columns by 32 row lanes (each every 32nd row), then the lanes in order.
-// A target's entry also goes to its first row's place in `side`, as in xent_epi_dweight.
-constexpr int kBiasCols = 64;
+// dbias of a piece: the column sums that the product which made d left for each 32 rows, added in
+// fp32 (read again from d itself, 134 MB a piece of 4096 rows, this took 18 us a piece). A block
+// takes 64 columns, 8 threads each: every 8th block of 32 rows, then the eight in order. A target's
+// entry also goes to its first row's place in `side`, as in xent_epi_dweight.
+constexpr int kBiasCols = 64, kBiasParts = 8;
 template <bool kF16>
-__global__ void __launch_bounds__(256)
-    xent_bias_kernel(const uint16_t* __restrict__ d, int32_t ld, int32_t cols, int32_t rows,
+__global__ void __launch_bounds__(kBiasCols* kBiasParts)
+    xent_bias_kernel(const float* __restrict__ part, int32_t pitch, int32_t cols, int32_t rows,
                      const int32_t* __restrict__ n_rows, const float* __restrict__ scale,
                      const int32_t* __restrict__ first, float* side, int32_t add,
                      uint16_t* d_bias) {
-  __shared__ float part[32][kBiasCols + 1];
+  __shared__ float s_part[kBiasParts][kBiasCols];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
   const int32_t n = n_rows != nullptr ? *n_rows : rows;
-  const int32_t cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
-  const int32_t c0 = (int32_t)blockIdx.x * kBiasCols;
-  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  // (a 64-column panel of d is whole in the buffer wherever one of its columns is)
-  const uint16_t* src = d + c0 + cg * 8;
+  const int col = (int)threadIdx.x % kBiasCols, k = (int)threadIdx.x / kBiasCols;
+  const int32_t c = (int32_t)blockIdx.x * kBiasCols + col;
+  float s = 0.0f;
+  // (a 64-column box of d is whole wherever one of its columns is)
 #pragma unroll 8
-  for (int32_t r = rl; r < n; r += 32) {
-    const uint4 q = *reinterpret_cast<const uint4*>(src + (int64_t)r * ld);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[2 * i] += unpack16<kF16>(w[i] & 0xffffu);
-      s[2 * i + 1] += unpack16<kF16>(w[i] >> 16);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[rl][cg * 8 + i] = s[i];
+  for (int32_t b = k; b < (n + 31) / 32; b += kBiasParts) s += part[(int64_t)b * pitch + c];
+  s_part[k][col] = s;
   __syncthreads();
-  if (threadIdx.x < kBiasCols && c0 + (int32_t)threadIdx.x < cols) {
-    float t = 0.0f;
-    for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
-    t = n > 0 ? t * scale[1] : 0.0f;
-    uint16_t* at = d_bias + c0 + threadIdx.x;
-    if (add) t += unpack16<kF16>(*at);
-    const int32_t r = first[c0 + threadIdx.x];
-    if (r != kXNoRow) side[r] = t;
-    *at = (uint16_t)(pack16<kF16>(t, 0.0f) & 0xffffu);
-  }
+  if (k > 0 || c >= cols) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kBiasParts; ++i) t += s_part[i][col];
+  t = n > 0 ? t * scale[1] : 0.0f;
+  uint16_t* at = d_bias + c;
+  if (add) t += unpack16<kF16>(*at);
+  const int32_t r = first[c];
+  if (r != kXNoRow) side[r] = t;
+  *at = (uint16_t)(pack16<kF16>(t, 0.0f) & 0xffffu);
 }
 
 }  // namespace lmh
