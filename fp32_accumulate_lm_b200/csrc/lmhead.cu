@@ -184,10 +184,12 @@ int current_device(DeviceInfo* out) {
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<4, false>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<1, true>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_bf16_f32_kernel<2, true>, d.smem_optin, nullptr) ||
-        !raise_smem_limit(lmh::xent_gemm_kernel<false, false>, d.smem_optin, nullptr) ||
-        !raise_smem_limit(lmh::xent_gemm_kernel<false, true>, d.smem_optin, nullptr) ||
-        !raise_smem_limit(lmh::xent_gemm_kernel<true, false>, d.smem_optin, nullptr) ||
-        !raise_smem_limit(lmh::xent_gemm_kernel<true, true>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXLone, false>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXLone, true>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXPair, false>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXPair, true>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXBig, false>, d.smem_optin, nullptr) ||
+        !raise_smem_limit(lmh::xent_gemm_kernel<lmh::kXBig, true>, d.smem_optin, nullptr) ||
         !raise_smem_limit(lmh::lmhead_w4a16_nvfp4_kernel<true>, d.smem_optin,
                           &d.nvfp4_static_smem[1]) ||
         !raise_smem_limit(lmh::lmhead_w4a16_nvfp4_kernel<false>, d.smem_optin,

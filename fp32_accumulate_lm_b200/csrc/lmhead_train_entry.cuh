@@ -170,6 +170,12 @@ int encode_xent(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// A matrix that is stored to, in the epilogues' boxes of 32 rows of 32 columns.
+int encode_xent_store(CUtensorMap* map, const void* base, int64_t cols, int64_t rows) {
+  return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, cols * 2, rows, 64, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 // The same matrix (cols a multiple of 64) seen as [cols / 64][rows][64], in boxes of 64 rows of
 // `blocks` column blocks.
 int encode_xent_mn(CUtensorMap* map, const void* base, int64_t cols, int64_t rows,
@@ -189,34 +195,58 @@ int encode_xent_mn(CUtensorMap* map, const void* base, int64_t cols, int64_t row
   return r == CUDA_SUCCESS ? LMHEAD_OK : LMHEAD_ERR_LAUNCH;
 }
 
-// Rows of B in one CTA's tile.
-uint32_t xent_b_rows(bool pair) {
-  return pair ? lmh::XentTile<true>::kBRows : lmh::XentTile<false>::kBRows;
-}
-
-int launch_xent_gemm(const DeviceInfo& dev, bool fp16, bool pair, const lmh::XentMaps& maps,
-                     lmh::XentParams p, lmhead_stream_t stream) {
-  int64_t tiles = 0;
-  for (int i = 0; i < p.n_problems; ++i) {
-    const lmh::XentProblem& q = p.prob[i];
-    const int64_t m = q.m_rows ? p.rows : q.m_len;
-    const int64_t tm = pair ? 256 : 128;
-    tiles += ((m + tm - 1) / tm) * ((q.n_len + lmh::kXN - 1) / lmh::kXN) * q.splits;
-  }
-  if ((tiles << 1) > kInt32Max) return LMHEAD_ERR_SHAPE;
-  const size_t smem = pair ? lmh::XentTile<true>::kSmem : lmh::XentTile<false>::kSmem;
-  if ((int64_t)smem > dev.smem_optin) return LMHEAD_ERR_SHAPE;
-  auto kernel = pair ? (fp16 ? lmh::xent_gemm_kernel<true, true> : lmh::xent_gemm_kernel<true, false>)
-                     : (fp16 ? lmh::xent_gemm_kernel<false, true>
-                             : lmh::xent_gemm_kernel<false, false>);
-  return launch_head(kernel, (unsigned)(tiles << (pair ? 1 : 0)), lmh::kXThreads, smem, stream,
-                     pair ? 2u : 1u, maps, p);
-}
+// How a call's products are tiled, and with it the boxes of the tensor maps.
+struct XentShape {
+  int shape;
+  // rows of an operand in one CTA's tile: A of the wide products; A of the weight product; B of the
+  // wide products; B of the weight product
+  uint32_t wide_a() const { return 128; }
+  uint32_t tall_a() const { return shape == lmh::kXBig ? 256 : 128; }
+  uint32_t wide_b() const { return shape == lmh::kXPair ? 128 : 256; }
+  uint32_t tall_b() const { return shape == lmh::kXLone ? 256 : 128; }
+};
 
 // CTA pairs for more than 128 rows. With at most 128 rows, half of a pair's 256-row tile would be
 // empty and the call is bound by reading W; lone CTAs of 128 rows spend half the tensor time.
-bool xent_pairs(const DeviceInfo& dev, int64_t rows) {
-  return rows > 128 && dev.pair_clusters > 0 && !g_no_cta_pairs.load(std::memory_order_relaxed);
+// Big tiles for the gradient of 2^28 logits or more: there they are 3 to 8 % faster (4096 rows x
+// 4096 x 151936: 11.89 ms against 12.71; 2048 x 2048: 3.17 against 3.26), with half as many logits 1
+// to 2 % slower on average (the waves of larger tiles fill the device worse, and a tile's epilogue is
+// in part exposed). The loss alone keeps pairs: its products have no output to write, and big tiles
+// measured 1 % faster at the largest sizes and up to 15 % slower elsewhere.
+XentShape xent_shape(const DeviceInfo& dev, int64_t rows, int64_t V, bool gradient) {
+  if (rows <= 128 || dev.pair_clusters <= 0 || g_no_cta_pairs.load(std::memory_order_relaxed))
+    return {lmh::kXLone};
+  return {gradient && rows * V >= (int64_t)1 << 28 ? lmh::kXBig : lmh::kXPair};
+}
+
+template <int kShape>
+int64_t xent_tiles(const lmh::XentParams& p) {
+  using T = lmh::XentTile<kShape>;
+  int64_t tiles = 0;
+  for (int i = 0; i < p.n_problems; ++i) {
+    const lmh::XentProblem& q = p.prob[i];
+    const int64_t m = q.m_rows ? p.rows : q.m_len, tm = T::rows(q.wide), tn = T::cols(q.wide);
+    tiles += ((m + tm - 1) / tm) * ((q.n_len + tn - 1) / tn) * q.splits;
+  }
+  return tiles;
+}
+
+template <int kShape>
+int launch_xent_shape(const DeviceInfo& dev, bool fp16, const lmh::XentMaps& maps,
+                      const lmh::XentParams& p, lmhead_stream_t stream) {
+  using T = lmh::XentTile<kShape>;
+  const int64_t ctas = xent_tiles<kShape>(p) * (T::kPair ? 2 : 1);
+  if (ctas > kInt32Max || (int64_t)T::kSmem > dev.smem_optin) return LMHEAD_ERR_SHAPE;
+  return launch_head(
+      fp16 ? lmh::xent_gemm_kernel<kShape, true> : lmh::xent_gemm_kernel<kShape, false>,
+      (unsigned)ctas, T::kThreads, T::kSmem, stream, T::kPair ? 2u : 1u, maps, p);
+}
+
+int launch_xent_gemm(const DeviceInfo& dev, bool fp16, XentShape s, const lmh::XentMaps& maps,
+                     const lmh::XentParams& p, lmhead_stream_t stream) {
+  return s.shape == lmh::kXBig    ? launch_xent_shape<lmh::kXBig>(dev, fp16, maps, p, stream)
+         : s.shape == lmh::kXPair ? launch_xent_shape<lmh::kXPair>(dev, fp16, maps, p, stream)
+                                  : launch_xent_shape<lmh::kXLone>(dev, fp16, maps, p, stream);
 }
 
 lmh::XentProblem xent_problem(int kind, int a_map, int b_map, int64_t n_len, int64_t k_len) {
@@ -227,6 +257,11 @@ lmh::XentProblem xent_problem(int kind, int a_map, int b_map, int64_t n_len, int
   q.n_len = (int32_t)n_len;
   q.k_len = (int32_t)k_len;
   q.splits = 1;
+  // M tiles walked together. The logits take 16, the rows' operands of a batch of 4096 staying in
+  // L2 while W streams by (4096 x 4096 x 128256: 3.34 ms, one at a time 3.96); the weight product
+  // one, d streaming by (3.39 ms, 16 at a time 3.57); dH's is the same within 1 % from 1 to 8.
+  q.group = kind == lmh::kXentDweight ? 1 : kind == lmh::kXentDhidden ? 4 : 16;
+  q.wide = kind != lmh::kXentDweight;
   return q;
 }
 
@@ -244,12 +279,12 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
     if (st != LMHEAD_OK) return st;
   }
-  const bool pair = xent_pairs(dev, rows);
+  const XentShape shape = xent_shape(dev, rows, V, false);
   lmh::XentMaps maps = {};
   st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
-                   ignoring ? round_up(rows, lmh::kBK) : rows, 128);
+                   ignoring ? round_up(rows, lmh::kBK) : rows, shape.wide_a());
   if (st != LMHEAD_OK) return st;
-  st = encode_xent(&maps.m[lmh::kMapW], W, H, V, xent_b_rows(pair));
+  st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
   if (st != LMHEAD_OK) return st;
 
   lmh::XentParams p = {};
@@ -259,13 +294,12 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   p.rows = (int32_t)rows;
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
-  p.group = 16;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
   p.targets = ignoring ? k.targets : targets;
   p.partials = f.partials;
   p.wait = wait_cfg();
-  st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
+  st = launch_xent_gemm(dev, fp16, shape, maps, p, stream);
   if (st != LMHEAD_OK) return st;
 
   const bool each = reduction == LMHEAD_REDUCE_NONE, mean = reduction == LMHEAD_REDUCE_MEAN;
@@ -294,7 +328,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   if (st != LMHEAD_OK) return st;
   const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
   const bool fp16 = dtype == LMHEAD_DTYPE_F16;
-  const bool pair = xent_pairs(dev, rows);
+  const XentShape shape = xent_shape(dev, rows, V, true);
   const XentPack& k = b.pack;
   if (ignoring) {
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
@@ -316,26 +350,28 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   // the forms of hidden and W as B's MN-major operand: in 3-D boxes, or where H is no multiple of
   // 64, in 2-D ones of 64 x 64
   const bool flat = H % 64 != 0;
-  const uint32_t b_rows = xent_b_rows(pair);
   const void* h = ignoring ? k.hidden : hidden;
   const int64_t h_rows = ignoring ? round_up(rows, lmh::kBK) : rows;
   lmh::XentMaps maps = {};
-  st = encode_xent(&maps.m[lmh::kMapHidden], h, H, h_rows, 128);
-  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, b_rows);
+  st = encode_xent(&maps.m[lmh::kMapHidden], h, H, h_rows, shape.wide_a());
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
   if (st == LMHEAD_OK)
     st = flat ? encode_xent(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, 64)
-              : encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, b_rows / 64);
+              : encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, shape.tall_b() / 64);
   if (st == LMHEAD_OK)
     st = flat ? encode_xent(&maps.m[lmh::kMapWMn], W, H, V, 64)
-              : encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, b_rows / 64);
+              : encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, shape.wide_b() / 64);
   for (int i = 0; i < 2 && st == LMHEAD_OK; ++i) {
-    st = encode_xent(&maps.m[lmh::kMapD + i], b.d[i], x.piece, x.rows_pad, 128);
+    st = encode_xent(&maps.m[lmh::kMapD + i], b.d[i], x.piece, x.rows_pad, shape.wide_a());
     if (st == LMHEAD_OK)
-      st = encode_xent_mn(&maps.m[lmh::kMapDMn + i], b.d[i], x.piece, x.rows_pad, 2);
+      st = encode_xent_mn(&maps.m[lmh::kMapDMn + i], b.d[i], x.piece, x.rows_pad, shape.tall_a() / 64);
     if (st == LMHEAD_OK)
-      st = encode_xent(&maps.m[lmh::kMapDStore + i], b.d[i], x.piece, x.rows_pad, 32);
+      st = encode_xent_store(&maps.m[lmh::kMapDStore + i], b.d[i], x.piece, x.rows_pad);
   }
-  if (st == LMHEAD_OK && d_W != nullptr) st = encode_xent(&maps.m[lmh::kMapDw], d_W, H, V, 32);
+  if (st == LMHEAD_OK && d_hidden != nullptr)
+    st = encode_2d(&maps.m[lmh::kMapDh], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, b.dh_partial, H,
+                   (int64_t)x.splits * x.rows_pad, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st == LMHEAD_OK && d_W != nullptr) st = encode_xent_store(&maps.m[lmh::kMapDw], d_W, H, V);
   if (st != LMHEAD_OK) return st;
 
   lmh::XentParams p = {};
@@ -343,7 +379,6 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
   p.rows_pad = (int32_t)x.rows_pad;
-  p.group = 16;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
   p.targets = ignoring ? k.targets : targets;
@@ -352,7 +387,6 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   p.row_info = b.row_info;
   p.scale = b.scale;
   p.d_weight = reinterpret_cast<uint16_t*>(d_W);
-  p.dh_partial = b.dh_partial;
   p.wait = wait_cfg();
 
   auto start = [&](int c) { return (int64_t)c * x.piece; };
@@ -369,7 +403,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   p.bias_part = d_bias != nullptr ? b.bias_part[0] : nullptr;
   p.n_problems = 1;
   p.prob[0] = logits_of(0);
-  st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
+  st = launch_xent_gemm(dev, fp16, shape, maps, p, stream);
   for (int c = 0; c < x.n_pieces && st == LMHEAD_OK; ++c) {
     if (d_bias != nullptr) {
       const unsigned blocks = (unsigned)((length(c) + lmh::kBiasCols - 1) / lmh::kBiasCols);
@@ -409,7 +443,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
       p.prob[p.n_problems++] = q;
     }
     if (c + 1 < x.n_pieces) p.prob[p.n_problems++] = logits_of(c + 1);
-    if (p.n_problems > 0) st = launch_xent_gemm(dev, fp16, pair, maps, p, stream);
+    if (p.n_problems > 0) st = launch_xent_gemm(dev, fp16, shape, maps, p, stream);
   }
   if (st != LMHEAD_OK) return st;
   lmh::XentFinishParams f = {};

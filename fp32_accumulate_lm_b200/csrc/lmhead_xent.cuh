@@ -41,7 +41,8 @@
 // on the device only; the tile walk reads it there.
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue, warp 10 tile scheduler (cluster launch
-// control, in launch order). No atomics on data and no split whose order varies: results are the
+// control, in launch order); with big tiles warps 10-17 are epilogue warps too and the scheduler is
+// warp 18. No atomics on data and no split whose order varies: results are the
 // same on every run.
 #pragma once
 
@@ -51,26 +52,43 @@ namespace lmh {
 
 constexpr int kXN = 256;                  // tile columns (MMA N)
 constexpr int kXBlock = 64 * 64 * 2;      // bytes of 64 K rows of 64 entries of M or N
-constexpr int kXEpiWarps = 8;
-constexpr int kXThreads = 64 + 32 * kXEpiWarps + 32;
+constexpr int kXEpiWarps = 8;             // epilogue warps of an accumulator
 constexpr int kXInfoSlots = 2;            // tile slots of the scheduler warp
 constexpr int kXAskAhead = 12;            // K steps before a tile's end at which the next is taken
-constexpr int kXStoreBox = 32 * 64 * 2;   // an epilogue warp's store box: 32 rows of 64 elements
+constexpr int kXStoreBox = 32 * 32 * 2;   // an epilogue warp's store box: 32 rows of 32 elements
 constexpr int kXMaxProblems = 3;
 constexpr int kXChunk = 128;              // vocab entries per (max, sum) pair of a row
 constexpr uint32_t kXTmemCols = 2 * kXN;
 constexpr int32_t kXNoRow = 0x7fffffff;
 
-template <bool kPair>
+// The shapes of a tile. A big tile is two accumulators of 256 x 256 on a CTA pair, side by side
+// along N where the product is `wide` (256 x 512) and along M elsewhere (512 x 256): a K step then
+// brings 48 KB into a CTA's shared memory for 1024 clocks of MMAs, and not 32 KB for 512. Under the
+// power cap the loads are what the tensor time is lost to: the weight product ran at 1190 TFLOP/s
+// with its loads and at 1750 with none (its MMAs on whatever lay there).
+enum : int { kXLone = 0, kXPair = 1, kXBig = 2 };
+
+template <int kShape>
 struct XentTile {
-  static constexpr int kM = kPair ? 256 : 128;                // tile rows
-  static constexpr int kBRows = kPair ? kXN / 2 : kXN;        // B rows in one CTA's shared memory
-  static constexpr int kABytes = 128 * 64 * 2;
+  static constexpr bool kPair = kShape != kXLone;
+  static constexpr bool kBig = kShape == kXBig;
+  static constexpr int kM = kPair ? 256 : 128;                // MMA rows
+  static constexpr int kRows = 128;                           // A rows in one CTA, per accumulator
+  static constexpr int kBRows = kPair ? kXN / 2 : kXN;        // B rows in one CTA, per accumulator
+  static constexpr int kABytes = kRows * 64 * 2;
   static constexpr int kBBytes = kBRows * 64 * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kPair ? 6 : 4;               // 192 KB either way
+  static constexpr int kStageBytes = kABytes + kBBytes + (kBig ? kABytes : 0);  // (A and B alike)
+  static constexpr int kStages = kShape == kXPair ? 6 : 4;    // 192 KB each way
+  // A big tile's accumulators have 8 epilogue warps each: TMEM is full, so the tensor pipe waits
+  // for whichever is read out last (with 8 warps for both in turn, the logits of 4096 x 1024 x
+  // 50304 took 371 us and not 356).
+  static constexpr int kEpiWarps = kBig ? 2 * kXEpiWarps : kXEpiWarps;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
   static constexpr size_t kSmem =
-      1024 + (size_t)kStages * kStageBytes + kXEpiWarps * kXStoreBox + 512;
+      1024 + (size_t)kStages * kStageBytes + kEpiWarps * kXStoreBox + 512;
+  // tile height and width of a product
+  __host__ __device__ static constexpr int rows(int wide) { return kBig && !wide ? 2 * kM : kM; }
+  __host__ __device__ static constexpr int cols(int wide) { return kBig && wide ? 2 * kXN : kXN; }
 };
 
 enum : int32_t {
@@ -80,7 +98,7 @@ enum : int32_t {
   kXentDhidden = 3,  // fp32 partial sums of dH, one buffer per split of K
 };
 
-// Tensor maps of one launch, all of them with 128-byte swizzle. A K-major operand is a 2-D matrix in
+// Tensor maps of one launch, those of loads with 128-byte swizzle. A K-major operand is a 2-D matrix in
 // boxes of 64 columns by all rows of a CTA's tile (128 of A, kBRows of B). An MN-major one comes as
 // a 3-D view [columns / 64][rows][64], a box being 64 rows of every 64-column block of the CTA's
 // tile. One box a stage and operand either way: with 64 x 64 boxes, two to four of them, the same
@@ -94,9 +112,10 @@ enum : int32_t {
   kMapWMn = 3,       // [V, H], MN-major
   kMapD = 4,         // the two d buffers [rows_pad, piece], K-major
   kMapDMn = 6,       // the same, MN-major
-  kMapDStore = 8,    // the same in boxes of 32 rows (stores)
-  kMapDw = 10,       // dW [V, H] in boxes of 32 rows (stores)
-  kMapCount = 11,
+  kMapDStore = 8,    // the same in boxes of 32 rows of 32 columns, 64-byte swizzle (stores)
+  kMapDw = 10,       // dW [V, H] in the same boxes (stores)
+  kMapDh = 11,       // the fp32 sums of dH [splits * rows_pad, H], boxes of 32 rows of 16 columns
+  kMapCount = 12,
 };
 struct XentMaps {
   CUtensorMap m[kMapCount];
@@ -113,6 +132,8 @@ struct XentProblem {
   int32_t b_off;          // first row of B's matrix (a piece of W starts at vocab entry b_off)
   int32_t b_k;            // 1: b_off is along K (dH: the piece's rows of W are B's K)
   int32_t splits;         // of K
+  int32_t group;          // M tiles walked together
+  int32_t wide;           // big tiles: 256 x 512 (else 512 x 256)
   int32_t out_off;        // first output row (dW: the piece's first vocab entry)
   int32_t add;            // dW: add to what is there; dH: add to the partial sums
 };
@@ -123,8 +144,7 @@ struct XentParams {
   int32_t rows;               // rows of hidden (the number that count when n_rows is null)
   const int32_t* n_rows;      // device: how many rows count, or null
   int32_t H;
-  int32_t rows_pad;           // row pitch of the dH partial buffers
-  int32_t group;              // M tiles walked together (their rows stay in L2)
+  int32_t rows_pad;           // rows of one split's sums of dH
   float alpha;
   const uint16_t* bias;       // [V] or null
   const int32_t* targets;     // [rows that count]
@@ -136,7 +156,6 @@ struct XentParams {
   int32_t* first;             // [V]: the first row whose target is this entry (kXNoRow: none)
   float* side;                // [rows that count][H]: dW's row of that target before its rounding
   uint16_t* d_weight;         // dW as memory, for add
-  float* dh_partial;          // [splits][rows_pad][H]
   WaitCfg wait;
 };
 
@@ -288,6 +307,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                "r"(src), "r"(x), "r"(y)
                : "memory");
 }
+// The same, added in fp32 to what is there.
+__device__ __forceinline__ void tma_add_2d_f32(const CUtensorMap* map, uint32_t src, int32_t x,
+                                               int32_t y) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], "
+      "[%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -335,10 +363,10 @@ struct XentTileAt {
 
 __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
 
-// The launch's tiles: the problems one after another, each split by split, M tiles in groups walked
-// N-major (a wave of tiles is then about as high as wide, and its operands fit L2). What does not
-// depend on the tile is worked out once: a tile's coordinates cost three 32-bit divisions.
-template <int kM>
+// The launch's tiles: the problems one after another, each split by split, M tiles in groups of the
+// problem's own number, N-major within a group. What does not depend on the tile is worked out once:
+// a tile's coordinates cost three 32-bit divisions.
+template <int kShape>
 struct XentWalk {
   int32_t mt[kXMaxProblems], nt[kXMaxProblems], ks[kXMaxProblems];
 
@@ -347,8 +375,8 @@ struct XentWalk {
     for (int i = 0; i < kXMaxProblems; ++i) {
       const XentProblem& q = p.prob[i];
       const bool used = i < p.n_problems;
-      mt[i] = used ? ceil_div(q.m_rows ? n_rows : q.m_len, kM) : 0;
-      nt[i] = used ? ceil_div(q.n_len, kXN) : 0;
+      mt[i] = used ? ceil_div(q.m_rows ? n_rows : q.m_len, XentTile<kShape>::rows(q.wide)) : 0;
+      nt[i] = used ? ceil_div(q.n_len, XentTile<kShape>::cols(q.wide)) : 0;
       ks[i] = used ? ceil_div(q.k_rows ? n_rows : q.k_len, kBK) : 0;
     }
   }
@@ -365,14 +393,15 @@ struct XentWalk {
         if (t < (int32_t)per * splits) {
           const uint32_t split = splits == 1 ? 0u : (uint32_t)t / per;
           const uint32_t u = (uint32_t)t - split * per;
-          const uint32_t group_tiles = (uint32_t)(p.group * nt[i]);
+          const int32_t group = p.prob[i].group, wide = p.prob[i].wide;
+          const uint32_t group_tiles = (uint32_t)(group * nt[i]);
           const uint32_t g = u / group_tiles;
           const uint32_t local = u - g * group_tiles;
-          const uint32_t gm = (uint32_t)min(p.group, mt[i] - (int32_t)g * p.group);
+          const uint32_t gm = (uint32_t)min(group, mt[i] - (int32_t)g * group);
           const uint32_t n = local / gm;
           c.prob = i;
-          c.m0 = ((int32_t)g * p.group + (int32_t)(local - n * gm)) * kM;
-          c.n0 = (int32_t)n * kXN;
+          c.m0 = ((int32_t)g * group + (int32_t)(local - n * gm)) * XentTile<kShape>::rows(wide);
+          c.n0 = (int32_t)n * XentTile<kShape>::cols(wide);
           c.split = (int32_t)split;
           // (at most 2^24 steps by 32 splits)
           c.k0 = splits == 1 ? 0 : (int32_t)((uint32_t)ks[i] * split / (uint32_t)splits);
@@ -549,37 +578,39 @@ __device__ __forceinline__ void xent_epi_stats(const XentParams& p, const XentPr
     __stcs(p.partials + (int64_t)(col / kXChunk) * p.rows + row, make_float2(m, s));
 }
 
-// The 64 columns of one store box, as 16-bit values in this warp's swizzled staging buffer.
+// The 32 columns of one store box, as 16-bit values in this warp's staging buffer: 32 rows of 64
+// bytes, with TMA's 64-byte swizzle (the 16-byte pieces of a row are permuted by its row pair).
 struct XentStage {
-  uint32_t buf;  // 32 rows of 128 bytes, 1024-byte aligned
-  __device__ __forceinline__ void begin() const {
-    if ((threadIdx.x & 31) == 0) bulk_wait_read();
-    __syncwarp();
-  }
-  // 32 columns: four 16-byte pieces, `half` 0 or 1 of the box
-  __device__ __forceinline__ void put(int half, const uint32_t (&w)[16]) const {
+  uint32_t buf;  // 1024-byte aligned
+  __device__ __forceinline__ void put(const uint32_t (&w)[16]) const {
     const uint32_t row = threadIdx.x & 31;
+    if (row == 0) bulk_wait_read();
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      st_shared_v4(buf + row * 128u + (((uint32_t)(half * 4 + j) ^ (row & 7u)) << 4), w[4 * j],
+      st_shared_v4(buf + row * 64u + (((uint32_t)j ^ ((row >> 1) & 3u)) << 4), w[4 * j],
                    w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
-  // The box's columns 2 * lane and 2 * lane + 1 summed over its 32 rows, in order.
+  // The sums of the box's columns 2 * i and 2 * i + 1 over its 32 rows, in lanes i and i + 16: the
+  // even rows, then the odd rows, each in order.
   template <bool kF16>
   __device__ __forceinline__ float2 column_sums() const {
-    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t pair = threadIdx.x & 15, odd = (threadIdx.x >> 4) & 1;
     __syncwarp();
     float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-    for (uint32_t row = 0; row < 32; ++row) {
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) {
+      const uint32_t row = 2 * i + odd;
       uint32_t w;
       asm volatile("ld.shared.b32 %0, [%1];"
                    : "=r"(w)
-                   : "r"(buf + row * 128u + (((lane >> 2) ^ (row & 7u)) << 4) + (lane & 3u) * 4u)
+                   : "r"(buf + row * 64u + (((pair >> 2) ^ (i & 3u)) << 4) + (pair & 3u) * 4u)
                    : "memory");
       s.x += unpack16<kF16>(w & 0xffffu);
       s.y += unpack16<kF16>(w >> 16);
     }
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, 16);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, 16);
     return s;
   }
   __device__ __forceinline__ void store(const CUtensorMap* map, int32_t x, int32_t y) const {
@@ -640,16 +671,13 @@ __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const Xent
     }
     uint32_t w[16];
     xent_pack32<kF16>(r, w);
-    if ((c & 32) == 0) st.begin();
-    st.put((c >> 5) & 1, w);
-    if (c & 32) {
-      const int32_t x = col + c - 32;
-      if (p.bias_part != nullptr) {
-        const float2 sums = st.column_sums<kF16>();
-        reinterpret_cast<float2*>(p.bias_part + (int64_t)(row0 / 32) * p.piece + x)[lane] = sums;
-      }
-      st.store(&maps.m[q.out_map], x, row0);
+    st.put(w);
+    if (p.bias_part != nullptr) {
+      const float2 sums = st.column_sums<kF16>();
+      float* at = p.bias_part + (int64_t)(row0 / 32) * p.piece + col + c;
+      if (lane < 16) reinterpret_cast<float2*>(at)[lane] = sums;
     }
+    st.store(&maps.m[q.out_map], col + c, row0);
   });
 }
 
@@ -664,8 +692,7 @@ __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const Xent
   const float scale = zero ? 0.0f : p.scale[1];  // (no row counts: 0, whatever the scale is)
   const bool add_row = q.add && row < q.m_len;
   const int64_t at = (int64_t)(q.out_off + row) * p.H;
-  const int32_t cols = min(kXChunk, (p.H - col + 63) / 64 * 64);
-  xent_columns(tacc, zero, cols, [&](int c, uint32_t(&r)[32]) {
+  xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
     const int32_t x = col + c;
 #pragma unroll
     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
@@ -693,34 +720,38 @@ __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const Xent
     }
     uint32_t w[16];
     xent_pack32<kF16>(r, w);
-    if ((c & 32) == 0) st.begin();
-    st.put((c >> 5) & 1, w);
+    st.put(w);
     // a box that starts past the piece's rows belongs to the next piece or to nothing
-    if ((c & 32) && row0 < q.m_len) st.store(&maps.m[q.out_map], x - 32, q.out_off + row0);
+    if (row0 < q.m_len) st.store(&maps.m[q.out_map], x, q.out_off + row0);
   });
 }
 
-// fp32 sums of dH over this piece's (and split's) vocab entries, added to the earlier pieces'.
+// fp32 sums of dH over this piece's (and split's) vocab entries, added to the earlier pieces' by
+// TMA: one addition an element and piece, in the order of the launches. (Read, added and written
+// by the threads, 16 bytes a lane of 32 rows at a time, a tile's epilogue took 80000 clocks, more
+// than the MMAs of 1024-wide pieces.) Rows that do not count are written too, and never read.
 __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const XentProblem& q,
+                                                 const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t split,
-                                                 int32_t row, bool row_ok, int32_t col) {
-  float* dst = p.dh_partial + ((int64_t)split * p.rows_pad + row) * p.H;
+                                                 int32_t row0, int32_t col) {
+  const CUtensorMap* map = &maps.m[kMapDh];
+  const int32_t y = split * p.rows_pad + row0;
   xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int32_t x = col + c + 4 * j;
-      if (row_ok && x < p.H) {
-        float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-        float4* a = reinterpret_cast<float4*>(dst + x);
-        if (q.add) {
-          const float4 o = *a;
-          v.x += o.x;
-          v.y += o.y;
-          v.z += o.z;
-          v.w += o.w;
-        }
-        *a = v;
+    for (int k = 0; k < 2; ++k) {
+      if (col + c + 16 * k >= p.H) break;
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = r[16 * k + j];
+      st.put(w);
+      fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {
+        if (q.add)
+          tma_add_2d_f32(map, st.buf, col + c + 16 * k, y);
+        else
+          tma_store_2d(map, st.buf, col + c + 16 * k, y);
+        bulk_commit();
       }
     }
   });
@@ -728,10 +759,11 @@ __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const Xent
 
 // ------------------------------------------------------------------ the kernel
 
-template <bool kPair, bool kF16>
-__global__ void __launch_bounds__(kXThreads, 1)
+template <int kShape, bool kF16>
+__global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
     xent_gemm_kernel(const __grid_constant__ XentMaps maps, const __grid_constant__ XentParams p) {
-  using T = XentTile<kPair>;
+  using T = XentTile<kShape>;
+  constexpr bool kPair = T::kPair, kBig = T::kBig;
   extern __shared__ uint8_t smem_raw[];
   if (threadIdx.x == 0) pdl_trigger();
   uint8_t* smem = align_up_1024(smem_raw);
@@ -742,7 +774,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const bool leader = rank == 0;
 
   uint8_t* staging = smem + (size_t)S * T::kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kXEpiWarps * kXStoreBox);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + T::kEpiWarps * kXStoreBox);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = smem_u32(bars + S);
   const uint32_t tfull0 = smem_u32(bars + 2 * S);
@@ -768,7 +800,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     for (int k = 0; k < kXInfoSlots; ++k) {
       mbar_init(info_ring.full0 + 8 * k, 1);
       // read by the producer, the epilogue warps and, in a pair's leader alone, the MMA warp
-      mbar_init(info_ring.empty0 + 8 * k, 1 + kXEpiWarps + (leader ? 1 : 0));
+      mbar_init(info_ring.empty0 + 8 * k, 1 + T::kEpiWarps + (leader ? 1 : 0));
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -822,9 +854,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
       const XentProblem& q = p.prob[tc.prob];
       const CUtensorMap* ma = &maps.m[q.a_map];
       const CUtensorMap* mb = &maps.m[q.b_map];
-      // this CTA's part of the tile: 128 rows of A, kBRows of B
-      const int32_t m0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0);
-      const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * T::kBRows : 0) + (q.b_k ? 0 : q.b_off);
+      // this CTA's part of the tile: its half of the rows of A and of B in a pair
+      const int32_t m0 = tc.m0 + (kPair ? (int32_t)rank * (T::rows(q.wide) / 2) : 0);
+      const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * (T::cols(q.wide) / 2) : 0) +
+                         (q.b_k ? 0 : q.b_off);
+      const uint32_t a_bytes = (kBig && !q.wide ? 2u : 1u) * T::kABytes;
+      const int b_blocks = (kBig && q.wide ? 2 : 1) * (T::kBRows / 64);
       for (int ks = 0; ks < tc.k_steps; ++ks) {
         if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, p.wait, abort_flag)) {
           fail(kRoleProducer, abort_flag);
@@ -835,7 +870,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (lane == 0 && !p.wait.starve_loads) {
           const uint32_t full = full0 + 8 * stage;
           const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
-          const uint32_t sb = sa + T::kABytes;
+          const uint32_t sb = sa + a_bytes;
           const int32_t k = (tc.k0 + ks) * kBK;
           const int32_t kb = k + (q.b_k ? q.b_off : 0);
           if (leader) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * T::kStageBytes);
@@ -848,8 +883,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
           } else if (!q.b_flat) {
             xent_load_3d<kPair>(sb, mb, full, n0, kb, pol);
           } else {
-#pragma unroll
-            for (int i = 0; i < T::kBRows / 64; ++i)
+            for (int i = 0; i < b_blocks; ++i)
               xent_load_2d<kPair>(sb + i * kXBlock, mb, full, n0 + 64 * i, kb, pol);
           }
         }
@@ -897,42 +931,104 @@ __global__ void __launch_bounds__(kXThreads, 1)
       // one K = 16 step further along: 32 bytes in a K-major tile, 16 rows in an MN-major one
       const uint64_t a_step = q.a_mn ? (16 * 128) >> 4 : 32 >> 4;
       const uint64_t b_step = q.b_mn ? (16 * 128) >> 4 : 32 >> 4;
-      if (!wait_bounded(tempty0 + 8 * acc, acc_phase ^ 1u, p.wait, abort_flag)) {
-        fail(kRoleMma, abort_flag);
-        break;
-      }
-      tc_fence_after_sync();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kXN);
-      for (int ks = 0; ks < tc.k_steps; ++ks) {
-        if (!wait_bounded(full0 + 8 * stage, phase, p.wait, abort_flag)) {
+      // accumulator h of the tile: of a big one both, else the one whose turn it is
+      auto acquire = [&](int h) {
+        if (!wait_bounded(tempty0 + 8 * h, acc_phase ^ 1u, p.wait, abort_flag)) return false;
+        tc_fence_after_sync();
+        return true;
+      };
+      auto filled = [&](int st, uint32_t ph) {
+        if (!wait_bounded(full0 + 8 * st, ph, p.wait, abort_flag)) return false;
+        tc_fence_after_sync();
+        return true;
+      };
+      auto multiply = [&](int st, int h, bool more) {
+        const uint32_t sa = smem_u32(smem + (size_t)st * T::kStageBytes);
+        const uint32_t sb = sa + (kBig && !q.wide ? 2u : 1u) * T::kABytes;
+        // the second accumulator's part of the operand that a big tile has two of
+        const uint32_t oa = kBig && !q.wide ? (uint32_t)h * T::kABytes : 0u;
+        const uint32_t ob = kBig && q.wide ? (uint32_t)h * T::kBBytes : 0u;
+        const uint64_t ad = q.a_mn ? sdesc_mnmajor_sw128(sa + oa) : sdesc_kmajor_sw128(sa + oa);
+        const uint64_t bd = q.b_mn ? sdesc_mnmajor_sw128(sb + ob) : sdesc_kmajor_sw128(sb + ob);
+        mma4_f16_steps_elect<kPair>(tmem_base + (uint32_t)(h * kXN), ad, bd, a_step, b_step, idesc,
+                                    more);
+      };
+      auto release = [&](uint32_t bar) {
+        if constexpr (kPair)
+          mma_commit_pair_elect(bar, 0x3);
+        else
+          mma_commit_elect(bar);
+        __syncwarp();
+      };
+      if constexpr (!kBig) {
+        if (!acquire(acc)) {
           fail(kRoleMma, abort_flag);
-          ok = false;
           break;
         }
-        tc_fence_after_sync();
-        const uint32_t sa = smem_u32(smem + (size_t)stage * T::kStageBytes);
-        const uint32_t sb = sa + T::kABytes;
-        const uint64_t ad = q.a_mn ? sdesc_mnmajor_sw128(sa) : sdesc_kmajor_sw128(sa);
-        const uint64_t bd = q.b_mn ? sdesc_mnmajor_sw128(sb) : sdesc_kmajor_sw128(sb);
-        mma4_f16_steps_elect<kPair>(d_tmem, ad, bd, a_step, b_step, idesc, ks != 0);
-        if constexpr (kPair)
-          mma_commit_pair_elect(empty0 + 8 * stage, 0x3);
-        else
-          mma_commit_elect(empty0 + 8 * stage);
-        __syncwarp();
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
+        for (int ks = 0; ks < tc.k_steps; ++ks) {
+          if (!filled(stage, phase)) {
+            ok = false;
+            break;
+          }
+          multiply(stage, acc, ks != 0);
+          release(empty0 + 8 * stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (!ok) {
+          fail(kRoleMma, abort_flag);
+          break;
+        }
+        release(tfull0 + 8 * acc);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      } else {
+        // Both accumulators of a big tile fill TMEM, so the epilogue of one runs under the MMAs of
+        // the other: the tile's first and last S steps go through all S stages for the first
+        // accumulator, then again for the second.
+        for (int ks = 0; ok && ks < tc.k_steps;) {
+          const int left = tc.k_steps - ks;
+          const int n = ks == 0 || left <= S ? min(S, left) : 1;
+          int st = stage;
+          uint32_t ph = phase;
+          if (ks == 0) ok = acquire(0);
+          for (int i = 0; ok && i < n; ++i) {
+            ok = filled(st, ph);
+            if (!ok) break;
+            multiply(st, 0, ks + i != 0);
+            if (++st == S) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+          if (ok && n == left) release(tfull0);
+          if (ok && ks == 0) ok = acquire(1);
+          for (int i = 0; ok && i < n; ++i) {
+            multiply(stage, 1, ks + i != 0);
+            release(empty0 + 8 * stage);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok && n == left) release(tfull0 + 8);
+          ks += n;
+        }
+        if (ok && tc.k_steps == 0) {
+          ok = acquire(0) && acquire(1);
+          if (ok) {
+            release(tfull0);
+            release(tfull0 + 8);
+          }
+        }
+        if (!ok) {
+          fail(kRoleMma, abort_flag);
+          break;
+        }
+        acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if constexpr (kPair)
-        mma_commit_pair_elect(tfull0 + 8 * acc, 0x3);
-      else
-        mma_commit_elect(tfull0 + 8 * acc);
-      __syncwarp();
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (leader) {
       if constexpr (kPair)
@@ -942,9 +1038,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
       __syncwarp();
       if (!wait_bounded(done_bar, 0, p.wait, nullptr)) fail(kRoleDrain, abort_flag);
     }
-  } else if (warp == 2 + kXEpiWarps) {
+  } else if (warp == 2 + T::kEpiWarps) {
     // ---------------------------------------------------------------- scheduler
-    const XentWalk<T::kM> walk(p, n_rows);
+    const XentWalk<kShape> walk(p, n_rows);
     int tile = (int)blockIdx.x >> (kPair ? 1 : 0);
     bool ok = true;
     int asked = 0;
@@ -977,7 +1073,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;      // TMEM lanes this warp may access
-    const int half = (warp - 2) >> 2;  // which 128 of the tile's columns
+    const int half = ((warp - 2) >> 2) & 1;  // which 128 of the accumulator's columns
     const XentStage st{smem_u32(staging + (warp - 2) * kXStoreBox)};
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -990,39 +1086,44 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (tc.prob == -2) break;
       if (tc.prob < 0) continue;
       const XentProblem& q = p.prob[tc.prob];
-      const int32_t row0 = tc.m0 + (kPair ? (int32_t)rank * 128 : 0) + quarter * 32;
+      // this warp's accumulator: its own of a big tile's two, else the one whose turn it is
+      const int h = kBig ? (warp - 2) / kXEpiWarps : acc;
+      // The rows and columns of its part of the accumulator. A big tile's accumulators are the
+      // halves of each CTA's A rows, or of its B rows: 128 columns of either CTA's.
+      int32_t row0 = tc.m0 + quarter * 32, col = tc.n0 + half * kXChunk;
+      if (kPair) row0 += (int32_t)rank * (T::rows(q.wide) / 2);
+      if (kBig && q.wide) col += half * kXChunk + h * kXChunk;
+      if (kBig && !q.wide) row0 += h * T::kRows;
       const int32_t row = row0 + lane;
       // what the row needs besides the sums, on its way during the wait
-      int32_t target = -1;
+      int32_t target = -1, first = kXNoRow;
       float4 info = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
-      if (q.kind == kXentStats && row < n_rows) target = p.targets[row];
+      if (!kBig && q.kind == kXentStats && row < n_rows) target = p.targets[row];
       if (q.kind == kXentDlogits && row < n_rows) info = p.row_info[row];
-      int32_t first = kXNoRow;
       if (q.kind == kXentDweight && row < q.m_len) first = p.first[q.out_off + row];
-      if (!wait_bounded(tfull0 + 8 * acc, acc_phase, p.wait, abort_flag, kSleepHintNs)) {
+      if (!wait_bounded(tfull0 + 8 * h, acc_phase, p.wait, abort_flag, kSleepHintNs)) {
         fail(kRoleEpilogue, abort_flag);
         break;
       }
       tc_fence_after_sync();
-      const int32_t col = tc.n0 + half * kXChunk;
       const bool zero = tc.k_steps == 0;
       const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                            (uint32_t)(acc * kXN + half * kXChunk);
-      if (q.kind == kXentStats)
+                            (uint32_t)(h * kXN + half * kXChunk);
+      if (!kBig && q.kind == kXentStats)  // (the loss takes no big tiles)
         xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
       else if (q.kind == kXentDlogits)
         xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, row < n_rows, info, col);
       else if (q.kind == kXentDweight)
         xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col);
       else
-        xent_epi_dhidden(p, q, tacc, zero, tc.split, row, row < n_rows, col);
+        xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, col);
       tc_fence_before_sync();
       if constexpr (kPair)
-        mbar_arrive_remote(tempty0 + 8 * acc, 0);
+        mbar_arrive_remote(tempty0 + 8 * h, 0);
       else
-        mbar_arrive(tempty0 + 8 * acc);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+        mbar_arrive(tempty0 + 8 * h);
+      if (!kBig) acc ^= 1;
+      if (kBig || acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_all();  // the stores have left this CTA's shared memory and landed
     __syncwarp();

@@ -93,6 +93,36 @@ def test_splits_of_the_vocabulary(rows, H, V):
     compare(*run_both(*make(rows, H, V, "f16"), reduction="sum"))
 
 
+@pytest.mark.parametrize("rows,H,V,dtype", [(2100, 72, 130001, "bf16"), (4097, 64, 65537, "f16"),
+                                            (16641, 136, 16200, "bf16"), (2048, 264, 131072, "f16")])
+def test_big_tiles(rows, H, V, dtype):
+    """2^28 logits and more take tiles of 256 x 512 and 512 x 256: ragged rows, vocabularies and
+    hidden sizes, masked rows, pieces, K shorter than the ring of stages and longer."""
+    assert rows * V >= 2 ** 28
+    hidden, W, targets, b, gl = make(rows, H, V, dtype, bias=True, masked=0.1)
+    loss, lse, grads, ref = run_both(hidden, W, targets, b, gl, z_loss=1e-4)
+    compare(loss, lse, grads, ref)
+    again = lm.cross_entropy_grad(hidden, W, targets, lse, gl, bias=b, z_loss=1e-4)
+    for a, c in zip(grads, again):
+        assert torch.equal(a, c)
+    base = grads[1].clone()
+    lm.cross_entropy_grad(hidden, W, targets, lse, gl, bias=b, z_loss=1e-4, accumulate=True,
+                          out=(None, base, None))
+    check_status()
+    twice = ref.d_W + grads[1].double()
+    assert_close(base, twice, ref.d_W_tol + 2.0 ** -7 * twice.abs(), "d_W, accumulated")
+
+
+def test_big_tiles_with_few_rows_that_count():
+    rows, H, V = 4096, 64, 65536
+    hidden, W, targets, b, gl = make(rows, H, V, masked=0.99)
+    compare(*run_both(hidden, W, targets, b, gl))
+    targets.fill_(IGNORE)
+    loss, lse, grads, ref = run_both(hidden, W, targets, b, gl)
+    for t in (loss, lse, grads[0], grads[1]):
+        assert torch.count_nonzero(t) == 0 and not torch.isnan(t).any()
+
+
 @pytest.mark.parametrize("wanted", [(0,), (1,), (2,), (0, 1), (1, 2), (0, 2), (0, 1, 2)])
 @pytest.mark.parametrize("rows", [60, 200])
 def test_gradients_wanted_and_accumulated(rows, wanted):
@@ -397,11 +427,11 @@ def test_the_gradient_against_differences():
 def test_starved_loads_time_out_cleanly():
     """Every wait of the products gives up after its limit, on lone CTAs and on pairs, and the next
     call is right."""
-    for rows in (30, 300):
-        hidden, W, targets, b, gl = make(rows, 128, 700)
+    for rows, V in ((30, 700), (300, 700), (2100, 130000)):  # lone CTAs, pairs, big tiles
+        hidden, W, targets, b, gl = make(rows, 64, V)
         with lm.test_hooks():
             lm.device_status(clear=True)
-            lm.set_fault_injection(True, wait_limit_ns=20_000_000)
+            lm.set_fault_injection(True, wait_limit_ns=5_000_000)
             try:
                 loss, lse = lm.cross_entropy_f32(hidden, W, targets)
                 lm.cross_entropy_grad(hidden, W, targets, lse, gl)
@@ -409,7 +439,7 @@ def test_starved_loads_time_out_cleanly():
             finally:
                 lm.set_fault_injection(False, 0)
             assert lm.device_status(clear=True) & 0xFF == lm.LMHEAD_ERR_TIMEOUT
-            lm.set_fault_injection(True, wait_limit_ns=20_000_000)
+            lm.set_fault_injection(True, wait_limit_ns=5_000_000)
             try:
                 with pytest.raises(lm.LmheadError):
                     lm.cross_entropy_f32(hidden, W, targets, check=True)
