@@ -198,9 +198,15 @@ int encode_xent_mn(CUtensorMap* map, const void* base, int64_t cols, int64_t row
 // How a call's products are tiled, and with it the boxes of the tensor maps.
 struct XentShape {
   int shape;
+  int64_t rows;
   // rows of an operand in one CTA's tile: A of the wide products; A of the weight product; B of the
   // wide products; B of the weight product
-  uint32_t wide_a() const { return 128; }
+  // (A: no more than there are, in whole swizzle atoms of 8. TMA is slow on rows past the matrix's
+  // end: one row in boxes of 128 took 335 us at 2048 x 151936, in boxes of 64 189 us, where 96 rows
+  // take 128 us.)
+  uint32_t wide_a() const {
+    return shape == lmh::kXLone && rows < 128 ? (uint32_t)round_up(rows, 8) : 128;
+  }
   uint32_t tall_a() const { return shape == lmh::kXBig ? 256 : 128; }
   uint32_t wide_b() const { return shape == lmh::kXPair ? 128 : 256; }
   uint32_t tall_b() const { return shape == lmh::kXLone ? 256 : 128; }
@@ -215,8 +221,8 @@ struct XentShape {
 // measured 1 % faster at the largest sizes and up to 15 % slower elsewhere.
 XentShape xent_shape(const DeviceInfo& dev, int64_t rows, int64_t V, bool gradient) {
   if (rows <= 128 || dev.pair_clusters <= 0 || g_no_cta_pairs.load(std::memory_order_relaxed))
-    return {lmh::kXLone};
-  return {gradient && rows * V >= (int64_t)1 << 28 ? lmh::kXBig : lmh::kXPair};
+    return {lmh::kXLone, rows};
+  return {gradient && rows * V >= (int64_t)1 << 28 ? lmh::kXBig : lmh::kXPair, rows};
 }
 
 template <int kShape>
@@ -292,6 +298,7 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   p.prob[0] = xent_problem(lmh::kXentStats, lmh::kMapHidden, lmh::kMapW, V, H);
   p.prob[0].m_rows = 1;
   p.rows = (int32_t)rows;
+  p.a_rows = (int32_t)shape.wide_a();
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
   p.alpha = alpha;
@@ -376,6 +383,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
 
   lmh::XentParams p = {};
   p.rows = (int32_t)rows;
+  p.a_rows = (int32_t)shape.wide_a();
   p.n_rows = k.n_rows;
   p.H = (int32_t)H;
   p.rows_pad = (int32_t)x.rows_pad;

@@ -145,6 +145,7 @@ struct XentParams {
   const int32_t* n_rows;      // device: how many rows count, or null
   int32_t H;
   int32_t rows_pad;           // rows of one split's sums of dH
+  int32_t a_rows;             // rows of a K-major A box (fewer than a CTA's 128: few rows in all)
   float alpha;
   const uint16_t* bias;       // [V] or null
   const int32_t* targets;     // [rows that count]
@@ -632,13 +633,15 @@ __device__ __forceinline__ void xent_pack32(const uint32_t (&r)[32], uint32_t (&
 
 // d of this thread's row over its 128 vocab entries of the piece, 16 bits, into the piece's buffer.
 // Rows that do not count and entries past V are written as 0: the products that read d take whole
-// 64-wide steps. The target's entry comes ready with the row's factors.
+// 64-wide steps. (Rows behind the last such step are not written.) The target's entry comes ready with the row's factors.
 template <bool kF16>
 __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t row0,
-                                                 int32_t row, bool row_ok, const float4& info,
+                                                 int32_t row, int32_t n_rows, const float4& info,
                                                  int32_t col) {
+  const bool row_ok = row < n_rows;
+  if (row0 >= (n_rows + kBK - 1) / kBK * kBK) return;  // the whole warp
   const int lane = threadIdx.x & 31;
   const int32_t V = q.b_off + q.n_len;  // the end of the piece as vocab ids
   const int32_t t = __float_as_int(info.w);
@@ -859,6 +862,10 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * (T::cols(q.wide) / 2) : 0) +
                          (q.b_k ? 0 : q.b_off);
       const uint32_t a_bytes = (kBig && !q.wide ? 2u : 1u) * T::kABytes;
+      // A K-major A box brings a_rows rows only; what lies below them in the tile is other rows' of
+      // the accumulator, and nobody reads those.
+      const uint32_t tx = (kPair ? 2u : 1u) * T::kStageBytes -
+                          (kPair || q.a_mn ? 0u : (uint32_t)(128 - p.a_rows) * 128u);
       const int b_blocks = (kBig && q.wide ? 2 : 1) * (T::kBRows / 64);
       for (int ks = 0; ks < tc.k_steps; ++ks) {
         if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, p.wait, abort_flag)) {
@@ -873,7 +880,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
           const uint32_t sb = sa + a_bytes;
           const int32_t k = (tc.k0 + ks) * kBK;
           const int32_t kb = k + (q.b_k ? q.b_off : 0);
-          if (leader) mbar_arrive_expect_tx(full, (kPair ? 2u : 1u) * T::kStageBytes);
+          if (leader) mbar_arrive_expect_tx(full, tx);
           if (q.a_mn)
             xent_load_3d<kPair>(sa, ma, full, m0, k, pol);
           else
@@ -1112,7 +1119,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (!kBig && q.kind == kXentStats)  // (the loss takes no big tiles)
         xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
       else if (q.kind == kXentDlogits)
-        xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, row < n_rows, info, col);
+        xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, n_rows, info, col);
       else if (q.kind == kXentDweight)
         xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col);
       else
