@@ -165,7 +165,9 @@ def load_test_library():
 
 
 def _active():
-    return load_test_library() if _use_test else load_library()
+    if _use_test:
+        return load_test_library()
+    return _lib if _lib is not None else load_library()
 
 
 @contextlib.contextmanager

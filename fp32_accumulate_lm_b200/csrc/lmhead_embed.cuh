@@ -86,15 +86,6 @@ struct EmbedSortParams {
   uint32_t* seen;             // [(V + 31) / 32] bits of the rows with a token, or null
 };
 
-// A word of another CTA's shared memory in the cluster, at the address of `p` in this one's.
-__device__ __forceinline__ int32_t cluster_load(const int32_t* p, uint32_t rank) {
-  uint32_t remote;
-  int32_t v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 // Cluster 0 sorts; the other clusters, if any, write zeros. keys are id - v_begin, or V for an id
 // outside the table, so those sort behind all others. Each CTA owns an eighth of the entries of a
 // pass, and takes them up to 8192 at a time, each warp a consecutive part: an entry's place is its

@@ -310,16 +310,16 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   if (st != LMHEAD_OK) return st;
 
   const bool each = reduction == LMHEAD_REDUCE_NONE, mean = reduction == LMHEAD_REDUCE_MEAN;
-  const bool one_block = rows <= lmh::kFoldRows;
+  const unsigned folds = (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows);
+  const bool one_cluster = !each && folds <= (unsigned)lmh::kFoldCluster;
   float* row_loss = each ? loss : f.row_loss;
   st = launch_head(fp16 ? lmh::xent_fold_kernel<true> : lmh::xent_fold_kernel<false>,
-                   (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows), 1024, 0, stream, 1u,
-                   (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
+                   folds, 1024, 0, stream, one_cluster ? folds : 1u, (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
                    (int32_t)rows, (int32_t)V, (const int32_t*)k.place, targets,
                    reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
                    (int32_t)(H / 8), p.bias, alpha, z_loss, row_loss, lse,
-                   (const int32_t*)k.n_rows, (int32_t)mean, !each && one_block ? loss : nullptr);
-  if (st != LMHEAD_OK || each || one_block) return st;
+                   (const int32_t*)k.n_rows, (int32_t)mean, one_cluster ? loss : nullptr);
+  if (st != LMHEAD_OK || each || one_cluster) return st;
   return launch_head(lmh::xent_reduce_kernel, 1, 1024, 0, stream, 1u, (const float*)row_loss,
                      (int32_t)rows, (const int32_t*)k.n_rows, (int32_t)mean, loss);
 }

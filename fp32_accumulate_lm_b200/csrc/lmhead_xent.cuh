@@ -223,6 +223,18 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// A word of another CTA's shared memory in the cluster, at the address of `p` in this one's.
+__device__ __forceinline__ int32_t cluster_load(const void* p, uint32_t rank) {
+  uint32_t remote;
+  int32_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+__device__ __forceinline__ float cluster_load_f32(const float* p, uint32_t rank) {
+  return __int_as_float(cluster_load(p, rank));
+}
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // One K step of 64 (four K = 16 MMAs, M rows across the pair for a pair) from a converged warp, one
@@ -1257,8 +1269,9 @@ __device__ __forceinline__ float xent_target_logit(const uint4* __restrict__ h,
 //   lse - z_t = log1p(s * 2^(m - x_t))                        where the target leads,
 //             = (m - x_t + log2(s + 2^(x_t - m))) / log2(e)   elsewhere,
 // so the loss of a row that is almost sure of its target keeps its bits. Ignored rows get 0 and 0;
-// a target outside [0, V) makes the row's loss NaN, and its lse is that of all entries. A launch of
-// a single block also adds the rows up (`total`), which saves the next launch.
+// a target outside [0, V) makes the row's loss NaN, and its lse is that of all entries. Where the
+// launch is a single cluster (at most 64 rows), its first block also adds the rows up in order
+// (`total`), which saves the next launch.
 __device__ __forceinline__ void xent_merge(float& m, float& s, float m2, float s2) {
   // NaN sums (a NaN or +inf logit) survive: exp of a NaN difference is NaN, and so is NaN * 0
   const float nm = fmaxf(m, m2);
@@ -1266,7 +1279,7 @@ __device__ __forceinline__ void xent_merge(float& m, float& s, float m2, float s
   s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
   m = nm;
 }
-constexpr int kFoldRows = 8, kFoldSegs = 128;
+constexpr int kFoldRows = 8, kFoldSegs = 128, kFoldCluster = 8;
 template <bool kF16>
 __global__ void __launch_bounds__(1024)
     xent_fold_kernel(const float2* __restrict__ partials, int32_t n_chunks, int32_t pitch,
@@ -1353,13 +1366,15 @@ __global__ void __launch_bounds__(1024)
   }
   if (total == nullptr) return;
   if (warp < kFoldRows && lane == 0) s_loss[warp] = loss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
+  cluster_sync_all();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     float sum = 0.0f;
+    for (uint32_t c = 0; c < gridDim.x; ++c)
 #pragma unroll
-    for (int i = 0; i < kFoldRows; ++i) sum += s_loss[i];
+      for (int i = 0; i < kFoldRows; ++i) sum += cluster_load_f32(&s_loss[i], c);
     *total = mean ? sum / (float)max(n_rows != nullptr ? *n_rows : rows, 1) : sum;
   }
+  cluster_sync_all();  // (the other blocks' sums have been read)
 }
 
 // The rows' losses added in a fixed order (each of 1024 threads every 1024th row, then a tree),
