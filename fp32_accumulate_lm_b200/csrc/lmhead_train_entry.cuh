@@ -310,10 +310,16 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   if (st != LMHEAD_OK) return st;
 
   const bool each = reduction == LMHEAD_REDUCE_NONE, mean = reduction == LMHEAD_REDUCE_MEAN;
-  const unsigned folds = (unsigned)((rows + lmh::kFoldRows - 1) / lmh::kFoldRows);
+  const bool few = rows < 2048;
+  const int64_t fold_rows = few ? lmh::kFoldFew : lmh::kFoldMany;
+  const unsigned folds = (unsigned)((rows + fold_rows - 1) / fold_rows);
   const bool one_cluster = !each && folds <= (unsigned)lmh::kFoldCluster;
   float* row_loss = each ? loss : f.row_loss;
-  st = launch_head(fp16 ? lmh::xent_fold_kernel<true> : lmh::xent_fold_kernel<false>,
+  auto fold = few ? (fp16 ? lmh::xent_fold_kernel<lmh::kFoldFew, true>
+                          : lmh::xent_fold_kernel<lmh::kFoldFew, false>)
+                  : (fp16 ? lmh::xent_fold_kernel<lmh::kFoldMany, true>
+                          : lmh::xent_fold_kernel<lmh::kFoldMany, false>);
+  st = launch_head(fold,
                    folds, 1024, 0, stream, one_cluster ? folds : 1u, (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
                    (int32_t)rows, (int32_t)V, (const int32_t*)k.place, targets,
                    reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),

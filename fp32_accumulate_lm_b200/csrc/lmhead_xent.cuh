@@ -1262,9 +1262,11 @@ __device__ __forceinline__ float xent_target_logit(const uint4* __restrict__ h,
 // ------------------------------------------------------------------ the loss from the statistics
 
 // Folds each row's (max, sum) pairs in a fixed order, joins the target's term and writes lse and the
-// row's loss. A block serves 8 rows: a quarter warp reads the pairs of its 8 rows (64 bytes) of one
-// chunk after another, 128 quarter warps take a segment of consecutive chunks each, and their
-// results are folded pairwise in order of the segments, a warp a row. With x = z * log2(e) and the
+// row's loss. The chunks are taken as 128 segments of consecutive ones, each folded in order, then
+// the segments in order, a warp a row. A block serves kRows rows, 8 or 32, and as many lanes read the
+// pairs of its rows of a chunk: 8 make four times the blocks, for few rows; 32 read 256 bytes at a
+// place and not 64, for many (8192 rows of 151936 entries: 62 us with 8 a block). The order, and so
+// every bit, is the same. With x = z * log2(e) and the
 // others' (m, s):
 //   lse - z_t = log1p(s * 2^(m - x_t))                        where the target leads,
 //             = (m - x_t + log2(s + 2^(x_t - m))) / log2(e)   elsewhere,
@@ -1279,8 +1281,8 @@ __device__ __forceinline__ void xent_merge(float& m, float& s, float m2, float s
   s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
   m = nm;
 }
-constexpr int kFoldRows = 8, kFoldSegs = 128, kFoldCluster = 8;
-template <bool kF16>
+constexpr int kFoldFew = 8, kFoldMany = 32, kFoldSegs = 128, kFoldCluster = 8;
+template <int kRows, bool kF16>
 __global__ void __launch_bounds__(1024)
     xent_fold_kernel(const float2* __restrict__ partials, int32_t n_chunks, int32_t pitch,
                      int32_t rows, int32_t V, const int32_t* __restrict__ place,
@@ -1289,38 +1291,37 @@ __global__ void __launch_bounds__(1024)
                      const uint16_t* __restrict__ bias, float alpha, float z_loss,
                      float* row_loss, float* lse_out, const int32_t* __restrict__ n_rows,
                      int32_t mean, float* total) {
-  __shared__ float2 seg[kFoldSegs][kFoldRows + 1];
-  __shared__ float s_loss[kFoldRows];
+  constexpr int kOwn = kFoldSegs * kRows / 1024;  // segments of a lane
+  __shared__ float2 seg[kFoldSegs][kRows + 1];
+  __shared__ float s_loss[kRows];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t r0 = (int32_t)blockIdx.x * kFoldRows;
+  const int32_t r0 = (int32_t)blockIdx.x * kRows;
   {
-    const int row = lane & 7, part = warp * 4 + (lane >> 3);
+    const int row = lane % kRows, part = (int)threadIdx.x / kRows;
     const int32_t r = r0 + row;
     const int32_t at = r >= rows ? -1 : place != nullptr ? place[r] : r;
     const int per_seg = (n_chunks + kFoldSegs - 1) / kFoldSegs;
-    const int c0 = part * per_seg, c1 = min(n_chunks, c0 + per_seg);
-    float m = -INFINITY, s = 0.0f;
-    if (at >= 0) {
-      int c = c0;
-      for (; c + 8 <= c1; c += 8) {
+#pragma unroll 1
+    for (int k = part * kOwn; k < (part + 1) * kOwn; ++k) {
+      const int c0 = k * per_seg, c1 = at >= 0 ? min(n_chunks, c0 + per_seg) : c0;
+      float m = -INFINITY, s = 0.0f;
+      for (int c = c0; c < c1; c += 8) {
         float2 q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = __ldcs(partials + (int64_t)(c + i) * pitch + at);
+        for (int i = 0; i < 8; ++i)
+          q[i] = c + i < c1 ? __ldcs(partials + (int64_t)(c + i) * pitch + at)
+                            : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) xent_merge(m, s, q[i].x, q[i].y);
       }
-      for (; c < c1; ++c) {
-        const float2 q = __ldcs(partials + (int64_t)c * pitch + at);
-        xent_merge(m, s, q.x, q.y);
-      }
+      seg[k][row] = make_float2(m, s);
     }
-    seg[part][row] = make_float2(m, s);
   }
   // the row's own warp: the target's logit, then the segments
   const int32_t r = r0 + warp;
-  const bool mine = warp < kFoldRows && r < rows;  // the whole warp
+  const bool mine = warp < kRows && r < rows;  // the whole warp
   const int32_t t = mine ? targets[r] : -1;
   const bool counts = mine && (place == nullptr || place[r] >= 0);
   const bool held = counts && t >= 0 && t < V;
@@ -1365,13 +1366,13 @@ __global__ void __launch_bounds__(1024)
     row_loss[r] = loss;
   }
   if (total == nullptr) return;
-  if (warp < kFoldRows && lane == 0) s_loss[warp] = loss;
+  if (warp < kRows && lane == 0) s_loss[warp] = loss;
   cluster_sync_all();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     float sum = 0.0f;
     for (uint32_t c = 0; c < gridDim.x; ++c)
 #pragma unroll
-      for (int i = 0; i < kFoldRows; ++i) sum += cluster_load_f32(&s_loss[i], c);
+      for (int i = 0; i < kRows; ++i) sum += cluster_load_f32(&s_loss[i], c);
     *total = mean ? sum / (float)max(n_rows != nullptr ? *n_rows : rows, 1) : sum;
   }
   cluster_sync_all();  // (the other blocks' sums have been read)

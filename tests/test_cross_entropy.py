@@ -297,6 +297,10 @@ def test_same_bits_every_time_and_rows_alone():
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
         for a, c in zip(lm.cross_entropy_grad(hidden, W, targets, lse, gl, **how), first):
             assert torch.equal(a, c)
+    # more rows than a block of the fold takes on another way
+    many = torch.arange(2400, device="cuda") % 600
+    big = lm.cross_entropy_f32(hidden[many], W, targets[many], **how)
+    assert torch.equal(big[0], loss[many]) and torch.equal(big[1], lse[many])
     for rows in (slice(0, 1), slice(5, 60), slice(100, 300), slice(599, 600)):
         part = lm.cross_entropy_f32(hidden[rows].contiguous(), W, targets[rows].contiguous(), **how)
         assert torch.equal(part[0], loss[rows]) and torch.equal(part[1], lse[rows])
