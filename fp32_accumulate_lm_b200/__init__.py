@@ -5,7 +5,10 @@
 ``logits_bf16_f32`` takes bf16 operands and returns fp32 logits (fp32 accumulation, alpha folded
 into the epilogue -- "[Model] Honor fp32 head_dtype in Inkling muP logits (target + MTP draft)",
 "muP is folded into the fp32 GEMM"); ``logits_w4a16_nvfp4`` is the W4A16 NVFP4 head with bf16
-logits (lm_head_nvfp4_rows.rs, lm_head_nvfp4_rows_run).
+logits (lm_head_nvfp4_rows.rs, lm_head_nvfp4_rows_run). For training, ``cross_entropy_f32`` and
+``cross_entropy_grad`` give the loss over the vocabulary and its gradient without keeping logits,
+``embedding`` and ``embedding_grad`` the token embedding of a tied table; ``linear_cross_entropy``
+and ``embed`` are the same as torch operations.
 
 This module only marshals arguments: every step of the computation runs in the CUDA library
 ``liblmhead.so`` built in-tree by ``fp32_accumulate_lm_b200._build``. If that library is

@@ -8,7 +8,8 @@
  * Entry 2 is the W4A16 NVFP4 head: E2M1 weights with per-16 E4M3 block scales and one fp32
  * per-tensor scale, bf16 activations that are never quantised, bf16 logits. Around them: the
  * log-probabilities of given tokens over the fp32 logits (whole vocabulary, or one vocab slice
- * per GPU plus a merge), and the NVFP4 quantiser.
+ * per GPU plus a merge), the NVFP4 quantiser, and for training the cross entropy over the
+ * vocabulary and the token embedding of a tied table, with their gradients.
  *
  * The operation comes from these pages:
  *  - "[Model] Honor fp32 head_dtype in Inkling muP logits (target + MTP draft)", "Purpose" and
@@ -30,14 +31,14 @@
  *  - Matrices are row-major and contiguous: hidden [rows, H], W [V, H] (used transposed), logits
  *    [rows, V].
  *  - A call validates its arguments synchronously on the host and launches nothing on error; it
- *    then enqueues its kernel (two for the log-probabilities and for the quantiser) on `stream`
- *    and returns without waiting. Faults surface at the caller's next synchronisation. There is
+ *    then enqueues its kernel (two for the log-probabilities and for the quantiser; see there for
+ *    the training entries) on `stream` and returns without waiting. Faults surface at the caller's next synchronisation. There is
  *    no fallback path of any kind.
  *  - rows == 0 is valid and launches nothing.
- *  - Determinism: the same inputs give the same bits on every run (no atomics, no split-K). Each
- *    output element is one fp32 accumulator chain over k in ascending 16-element steps, the same
- *    for every row count, row position and tile, so a row's logits are bit-identical whether it
- *    is computed alone or with any other rows.
+ *  - Determinism: the same inputs give the same bits on every run. Each logit is one fp32
+ *    accumulator chain over k in ascending 16-element steps (no atomics, no split-K), the same for
+ *    every row count, row position and tile, so a row's logits are bit-identical whether it is
+ *    computed alone or with any other rows.
  *  - Outputs must not overlap inputs (LMHEAD_ERR_ALIAS).
  *  - Functions are thread-safe; calls on different streams may run concurrently.
  */
@@ -302,8 +303,10 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * d_bias then. The products take dz in the operands' 16-bit type (each entry off by at most half a
  * step of that type, fp16 with a common power of two taken out); every sum is fp32.
  *
- * Both are deterministic. The loss of a row does not depend on the other rows of the call; the
- * gradients' sums run over the rows that count in order.
+ * Both are deterministic. The loss and lse of a row do not depend on the other rows of the call, bit
+ * for bit; the gradients' sums run over the rows that count in order. The target's logit is summed in
+ * fp32 outside the tensor cores, whose accumulator truncates; so losses are not the negatives of
+ * lmhead_logprobs_f32's results to the last bit, but closer to the exact ones.
  *
  *   hidden, W, bias, dtype, alpha: as lmhead_logits_f32; d_hidden, d_W 16-byte aligned, d_bias 2
  *   targets    int32 [rows], 4-byte aligned
@@ -313,8 +316,8 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  *   sizes      rows, H, V < 2^30
  * rows == 0: the loss of REDUCE_SUM and REDUCE_MEAN is written as 0, and so are d_W and d_bias unless
  * they accumulate. Outputs and the workspace must not overlap each other or the inputs. The first
- * enqueues three to four kernels, the second four to five and one more for each piece of the
- * vocabulary. Each returns an lmhead_status.
+ * enqueues two to four kernels; the second three or four, and for each piece of the vocabulary one,
+ * or two with d_bias. Each returns an lmhead_status.
  */
 #define LMHEAD_IGNORE_NONE INT64_MIN
 typedef enum {
