@@ -7,8 +7,8 @@
 //
 // with a_r = 1 + 2 z_loss lse_r and b_r = 1 where every row has the same upstream gradient g (then
 // scale = alpha * g / rows that count), or both times g_r where each row has its own (scale =
-// alpha). So with one upstream gradient the target's entry of a row is p - 1, which bf16 holds to
-// 2^-9 of a number near 1, and g itself is never rounded to 16 bits. A power of two 2^k joins a_r
+// alpha). So with one upstream gradient the target's entry of a row is p - 1, and g itself is never
+// rounded to 16 bits. A power of two 2^k joins a_r
 // and b_r and leaves again with `scale`, so that the largest factor lies in [2^13, 2^14): fp16 has
 // 2^-28 of the largest entry as its smallest normal number then (softmax values of 1e-8 keep all
 // their bits), and 2^15, the most an entry can reach, stays below its 65504. bf16 takes the same
@@ -16,8 +16,9 @@
 //
 // Why d is rounded to the operands' 16-bit type: it is the operand of two tensor-core products
 // whose other operand has that type (one MMA never mixes types). Each rounding is off by at most
-// half a step (2^-9 relative in bf16, 2^-12 in fp16), independently from entry to entry; the sums
-// over the vocabulary and over the rows are fp32, and the gradients leave in that type anyway.
+// half a step (2^-8 relative in bf16, 2^-11 in fp16), independently from entry to entry; the sums
+// over the vocabulary and over the rows are fp32, and the gradients leave in that type anyway. The
+// one entry whose error does not average out, the target's, is mended in fp32 (xent_finish_kernel).
 //
 // Four products of 2 rows V H operations each: the logits for the loss, the logits again for the
 // gradient (they are not kept), and the two gradients. The vocabulary is taken in pieces: the
@@ -26,14 +27,13 @@
 // two gradient products of piece c and the logits of piece c + 1, so the device drains once a
 // piece and not three times.
 //
-// All products are one kernel, xent_gemm_kernel: C[M, N] = A[M, K] B[N, K]^T in tiles of 256 x 256
-// on CTA pairs (128 x 256 on lone CTAs), operands by TMA as 64 x 64 boxes of 128-byte-swizzled
-// rows, fp32 accumulators in TMEM (two of 256 columns, so that the epilogue of a tile runs under
-// the MMAs of the next). An operand whose K runs along its rows in memory is a K-major tile of
-// 8-row atoms; one whose K runs down the columns (h and d in dW = d^T h, W in dH = d W) is the same
-// boxes read as an MN-major tile: 64 entries of M or N by 8 of K per atom. So nothing is ever
-// transposed in memory. A TMEM lane holds a row of the tile: a thread has 128 logits of one row in
-// turn, and the softmax statistics need no exchange between lanes.
+// All products are one kernel, xent_gemm_kernel: C[M, N] = A[M, K] B[N, K]^T, operands by TMA in
+// boxes of 128-byte-swizzled rows, fp32 accumulators in TMEM (two, so that the epilogue of a tile
+// runs under the MMAs of the next). An operand whose K runs along its rows in memory is a K-major
+// tile of 8-row atoms; one whose K runs down the columns (h and d in dW = d^T h, W in dH = d W) is
+// read as an MN-major tile, 64 entries of M or N by 8 of K an atom. So nothing is ever transposed in
+// memory. A TMEM lane holds a row of the tile: a thread has 128 logits of one row in turn, and the
+// softmax statistics need no exchange between lanes.
 //
 // Rows whose target is ignored are taken out first (xent_pack_kernel): the rows that count are
 // copied side by side, and every product runs over those alone. Masked rows cost no tensor time,
@@ -42,15 +42,15 @@
 //
 // Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue, warp 10 tile scheduler (cluster launch
 // control, in launch order); with big tiles warps 10-17 are epilogue warps too and the scheduler is
-// warp 18. No atomics on data and no split whose order varies: results are the
-// same on every run.
+// warp 18. Results are the same on every run: no split's order varies, an element of dH is added to
+// once a launch, and the only atomics are minima of row numbers.
 #pragma once
 
 #include "lmhead_bf16.cuh"
 
 namespace lmh {
 
-constexpr int kXN = 256;                  // tile columns (MMA N)
+constexpr int kXN = 256;                  // accumulator columns (MMA N)
 constexpr int kXBlock = 64 * 64 * 2;      // bytes of 64 K rows of 64 entries of M or N
 constexpr int kXEpiWarps = 8;             // epilogue warps of an accumulator
 constexpr int kXInfoSlots = 2;            // tile slots of the scheduler warp
@@ -61,7 +61,8 @@ constexpr int kXChunk = 128;              // vocab entries per (max, sum) pair o
 constexpr uint32_t kXTmemCols = 2 * kXN;
 constexpr int32_t kXNoRow = 0x7fffffff;
 
-// The shapes of a tile. A big tile is two accumulators of 256 x 256 on a CTA pair, side by side
+// The shapes of a tile: 128 x 256 on a lone CTA, 256 x 256 on a CTA pair, and the big ones. A big
+// tile is two accumulators of 256 x 256 on a CTA pair, side by side
 // along N where the product is `wide` (256 x 512) and along M elsewhere (512 x 256): a K step then
 // brings 48 KB into a CTA's shared memory for 1024 clocks of MMAs, and not 32 KB for 512. Under the
 // power cap the loads are what the tensor time is lost to: the weight product ran at 1190 TFLOP/s
@@ -98,11 +99,11 @@ enum : int32_t {
   kXentDhidden = 3,  // fp32 partial sums of dH, one buffer per split of K
 };
 
-// Tensor maps of one launch, those of loads with 128-byte swizzle. A K-major operand is a 2-D matrix in
-// boxes of 64 columns by all rows of a CTA's tile (128 of A, kBRows of B). An MN-major one comes as
+// Tensor maps of one launch, those of loads with 128-byte swizzle. A K-major operand is a 2-D matrix
+// in boxes of 64 columns by all rows of a CTA's tile (128 of A, kBRows of B). An MN-major one comes as
 // a 3-D view [columns / 64][rows][64], a box being 64 rows of every 64-column block of the CTA's
 // tile. One box a stage and operand either way: with 64 x 64 boxes, two to four of them, the same
-// loads fed the tensor cores at 1150 TFLOP/s and not at 1325 (8192 x 4096 x 128256 logits under
+// loads fed the tensor cores at 1150 TFLOP/s and not at 1325 (4096 x 4096 x 128256 logits under
 // the power cap). Where H is no multiple of 64 the 3-D view of hidden and W does not exist, and
 // their MN-major tiles come as 64 x 64 boxes of the 2-D matrix.
 enum : int32_t {
@@ -473,6 +474,7 @@ __device__ __forceinline__ bool xent_read(const XentInfo& f, int j, XentTileAt& 
   // the same in every lane, and the compiler may know it
   c.prob = __shfl_sync(0xffffffffu, c.prob, 0);
   c.k_steps = __shfl_sync(0xffffffffu, c.k_steps, 0);
+  __syncwarp();  // every lane has read the slot
   if ((threadIdx.x & 31) == 0) mbar_arrive(f.empty0 + 8 * k);
   __syncwarp();
   return true;
@@ -481,10 +483,11 @@ __device__ __forceinline__ bool xent_read(const XentInfo& f, int j, XentTileAt& 
 // ------------------------------------------------------------------ epilogues
 // Each is called by one warp with its 32 rows of the tile (row = its lane's) and its 128 columns
 // from `col`; `tacc` addresses the first of them in TMEM; `zero` says that K was empty and the
-// accumulator was never written. Columns come 32 at a time. The two softmax epilogues work in units of log 2 (z * log2(e), one multiply for
-// alpha and the change of base) on pairs of values: at 1024-wide hidden rows a tile's MMAs take
-// about 8000 clocks and 128 x 256 exponentials 2000 of the SM's special-function unit, but one
-// instruction at a time (some 18 an entry) the epilogue took 15000 and held the tensor pipe up.
+// accumulator was never written. Columns come 32 at a time. The two softmax epilogues work in units
+// of log 2 (z * log2(e), one multiply for alpha and the change of base) on pairs of values: at
+// 1024-wide hidden rows a tile's MMAs take about 8000 clocks and 128 x 256 exponentials 2000 of the
+// SM's special-function unit, but one instruction at a time (some 18 an entry) the epilogue took
+// 15000 and held the tensor pipe up.
 
 __device__ __forceinline__ void xent_acc_load(uint32_t tacc, bool zero, uint32_t (&r)[32]) {
   __syncwarp();  // the lanes may come from rows of their own; the TMEM load is the warp's
@@ -645,7 +648,8 @@ __device__ __forceinline__ void xent_pack32(const uint32_t (&r)[32], uint32_t (&
 
 // d of this thread's row over its 128 vocab entries of the piece, 16 bits, into the piece's buffer.
 // Rows that do not count and entries past V are written as 0: the products that read d take whole
-// 64-wide steps. (Rows behind the last such step are not written.) The target's entry comes ready with the row's factors.
+// 64-wide steps. (Rows behind the last such step are not written.) The target's entry comes ready
+// with the row's factors.
 template <bool kF16>
 __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
@@ -1352,8 +1356,9 @@ __global__ void __launch_bounds__(1024)
         lse = zt + loss;
       } else {
         const float l = log2f(s + exp2f(xt - m));
-        loss = (m - xt + l) * kLn2;
         lse = (m + l) * kLn2;
+        // (a target near the lowest fp32 value, taken out by its bias: x_t is past it)
+        loss = xt > -INFINITY ? (m - xt + l) * kLn2 : lse - zt;
       }
     } else {
       lse = (m + log2f(s)) * kLn2;

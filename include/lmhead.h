@@ -286,9 +286,9 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * A row whose target is `ignore_index` does not count: its loss and lse are 0, and nothing that its
  * hidden row holds (NaN, infinities) reaches any output. With no row that counts the sum and the
  * mean are 0. ignore_index = LMHEAD_IGNORE_NONE says that every row counts, which saves a copy of
- * the hidden rows. Any other target outside [0, V) makes the row's loss NaN. z may be -inf (a bias
- * of -inf takes an entry out of the vocabulary), as long as a row has one finite logit; a NaN or
- * +inf logit makes the row's loss and lse NaN.
+ * the hidden rows. Any other target outside [0, V) makes the row's loss NaN. z may be -inf or very
+ * low (a bias of -inf, or of the type's lowest value, takes an entry out of the vocabulary), as long
+ * as a row has one logit of ordinary size; a NaN or +inf logit makes the row's loss and lse NaN.
  *
  * lmhead_cross_entropy_grad gives the gradients for the upstream gradient `grad_loss` (fp32 [rows]
  * for LMHEAD_REDUCE_NONE, else one fp32), recomputing the logits from hidden and W:
@@ -314,6 +314,7 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  *   loss       fp32 [rows] or [1], grad_loss likewise, 4-byte aligned
  *   workspace  at least the *_workspace_bytes of the same sizes, 256-byte aligned
  *   sizes      rows, H, V < 2^30
+ * A workspace serves one call at a time: not two that may run at once, as graphs or on streams.
  * rows == 0: the loss of REDUCE_SUM and REDUCE_MEAN is written as 0, and so are d_W and d_bias unless
  * they accumulate. Outputs and the workspace must not overlap each other or the inputs. The first
  * enqueues two to four kernels; the second three or four, and for each piece of the vocabulary one,
@@ -361,8 +362,8 @@ int lmhead_cross_entropy_grad(const void* hidden, int dtype, int64_t rows, int64
  *   W, d_W   dtype [V, H], 16-byte aligned            H > 0, H % 8 == 0, V > 0
  *   out, d_out  dtype [tokens, H], 16-byte aligned    v_begin >= 0, v_begin + V <= 2^31
  *   workspace   at least lmhead_embedding_grad_workspace_bytes(tokens, V, H) bytes, 256-byte aligned
- *   tokens, H, V < 2^30
- * Outputs and the workspace must not overlap each other or the inputs. The first enqueues one
+ *   tokens, H, V < 2^30; H <= 2^24 for the gradient
+ * A workspace serves one call at a time. Outputs and the workspace must not overlap each other or the inputs. The first enqueues one
  * kernel, the second two or three (tokens == 0 writes zeros, or nothing when it accumulates). Each
  * returns an lmhead_status.
  */

@@ -218,9 +218,12 @@ def test_entries_taken_out_by_the_bias(rows):
     b[600:640] = torch.finfo(b.dtype).min
     targets[:] = torch.randint(0, 130, (rows,), device="cuda", dtype=torch.int32)
     targets[3] = 200
+    targets[5] = 620
     loss, lse, grads, ref = run_both(hidden, W, targets, b, gl, reduction="none")
     keep = torch.arange(rows, device="cuda") != 3
     assert loss[3] == float("inf")
+    # (the bound of z at the lowest value is that of its own rounding)
+    ref.loss_tol[5] = 2.0 ** -22 * ref.loss[5]
     assert_close(loss[keep], ref.loss[keep], ref.loss_tol[keep], "loss")
     assert_close(lse, ref.lse, ref.lse_tol, "lse")
     for g in grads:
@@ -257,6 +260,42 @@ def test_rows_sure_of_their_target():
     eps_lse = 2.0 ** -24 * ref.lse.abs() / ref.loss.clamp(max=1)  # lse travels as fp32
     bound = 2 * 2.0 ** -8 + 8 * size * H * 2.0 ** -24 + 2 * eps_lse
     assert (off <= bound).all(), float((off / bound).max())
+
+
+def test_a_table_of_more_than_2_31_elements():
+    """Offsets past 32 bits in W and d_W: targets and ids at the table's end, checked there."""
+    rows, H, V = 140, 16384, 140000
+    assert V * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(5)
+    W = torch.empty(V, H, device="cuda", dtype=torch.bfloat16)
+    for v in range(0, V, 20000):
+        W[v:v + 20000] = torch.randn((20000, H), generator=g, device="cuda") * 0.005
+    hidden = torch.randn((rows, H), generator=g, device="cuda").bfloat16()
+    targets = (V - 1 - torch.arange(rows, device="cuda") * 3).to(torch.int32)
+    loss, lse = lm.cross_entropy_f32(hidden, W, targets, reduction="none", ignore_index=None)
+    up = torch.ones(rows, device="cuda")
+    d_hidden, d_W, _ = lm.cross_entropy_grad(hidden, W, targets, lse, up, reduction="none",
+                                             ignore_index=None)
+    check_status()
+    z = torch.cat([hidden.double() @ W[v:v + 20000].double().t() for v in range(0, V, 20000)], 1)
+    tol = (hidden.double().abs() * 0.03).sum(1) * 1e-4 + 1e-5
+    want = torch.logsumexp(z, 1)
+    assert_close(lse, want, tol, "lse")
+    assert_close(loss, want - z.gather(1, targets.long()[:, None])[:, 0], 2 * tol, "loss")
+    p = torch.exp(z - want[:, None])
+    p[torch.arange(rows, device="cuda"), targets.long()] -= 1.0
+    last = V - 600  # the rows of all targets
+    want = p[:, last:].t() @ hidden.double()
+    size = p[:, last:].abs().t() @ hidden.double().abs()
+    assert_close(d_W[last:], want, size * (2.0 ** -8 + 2 * float(tol.max())) + 2.0 ** -8 * want.abs(), "d_W")
+    x = lm.embedding(targets, W)
+    assert torch.equal(x, W[targets.long()])
+    lm.embedding_grad(x, targets, V, out=d_W)
+    check_status()
+    assert torch.equal(d_W[targets.long()], x)
+    seen = torch.zeros(V, dtype=torch.bool, device="cuda")
+    seen[targets.long()] = True
+    assert not d_W[~seen].any()
 
 
 def test_nan_and_inf_in_rows_that_count():
