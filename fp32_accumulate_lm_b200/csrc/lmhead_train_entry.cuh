@@ -374,7 +374,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   if (st == LMHEAD_OK)
     st = flat ? encode_xent(&maps.m[lmh::kMapWMn], W, H, V, 64)
               : encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, shape.wide_b() / 64);
-  for (int i = 0; i < 2 && st == LMHEAD_OK; ++i) {
+  for (int i = 0; i < (x.n_pieces > 1 ? 2 : 1) && st == LMHEAD_OK; ++i) {
     st = encode_xent(&maps.m[lmh::kMapD + i], b.d[i], x.piece, x.rows_pad, shape.wide_a());
     if (st == LMHEAD_OK)
       st = encode_xent_mn(&maps.m[lmh::kMapDMn + i], b.d[i], x.piece, x.rows_pad, shape.tall_a() / 64);
