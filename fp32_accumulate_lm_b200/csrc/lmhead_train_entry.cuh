@@ -70,9 +70,13 @@ struct XentForward {
 
 int64_t xent_chunks(int64_t V) { return (V + lmh::kXChunk - 1) / lmh::kXChunk; }
 
+// Ignored rows are taken out of the loss's product where that saves a tile; what they hold meets no
+// other row there. (The gradient always takes them out.)
+bool xent_loss_packs(int64_t rows, bool ignoring) { return ignoring && rows > 128; }
+
 XentForward carve_forward(Carver& c, int64_t rows, int64_t H, int64_t V, bool ignoring) {
   XentForward f;
-  f.pack = carve_pack(c, rows, H, ignoring);
+  f.pack = carve_pack(c, rows, H, xent_loss_packs(rows, ignoring));
   f.partials = c.take<float2>(xent_chunks(V) * rows);
   f.row_loss = c.take<float>(rows);
   return f;
@@ -279,16 +283,17 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   int st = current_device(&dev);
   if (st != LMHEAD_OK) return st;
   const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
+  const bool packing = xent_loss_packs(rows, ignoring);
   const bool fp16 = dtype == LMHEAD_DTYPE_F16;
   const XentPack& k = f.pack;
-  if (ignoring) {
+  if (packing) {
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
     if (st != LMHEAD_OK) return st;
   }
   const XentShape shape = xent_shape(dev, rows, V, false);
   lmh::XentMaps maps = {};
-  st = encode_xent(&maps.m[lmh::kMapHidden], ignoring ? k.hidden : hidden, H,
-                   ignoring ? round_up(rows, lmh::kBK) : rows, shape.wide_a());
+  st = encode_xent(&maps.m[lmh::kMapHidden], packing ? k.hidden : hidden, H,
+                   packing ? round_up(rows, lmh::kBK) : rows, shape.wide_a());
   if (st != LMHEAD_OK) return st;
   st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
   if (st != LMHEAD_OK) return st;
@@ -303,7 +308,7 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   p.H = (int32_t)H;
   p.alpha = alpha;
   p.bias = reinterpret_cast<const uint16_t*>(bias);
-  p.targets = ignoring ? k.targets : targets;
+  p.targets = packing ? k.targets : targets;
   p.partials = f.partials;
   p.wait = wait_cfg();
   st = launch_xent_gemm(dev, fp16, shape, maps, p, stream);
@@ -319,15 +324,17 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
                           : lmh::xent_fold_kernel<lmh::kFoldFew, false>)
                   : (fp16 ? lmh::xent_fold_kernel<lmh::kFoldMany, true>
                           : lmh::xent_fold_kernel<lmh::kFoldMany, false>);
-  st = launch_head(fold,
-                   folds, 1024, 0, stream, one_cluster ? folds : 1u, (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
+  st = launch_head(fold, folds, 1024, 0, stream, one_cluster ? folds : 1u,
+                   (const float2*)f.partials, (int32_t)xent_chunks(V), (int32_t)rows,
                    (int32_t)rows, (int32_t)V, (const int32_t*)k.place, targets,
                    reinterpret_cast<const uint4*>(hidden), reinterpret_cast<const uint4*>(W),
                    (int32_t)(H / 8), p.bias, alpha, z_loss, row_loss, lse,
-                   (const int32_t*)k.n_rows, (int32_t)mean, one_cluster ? loss : nullptr);
+                   (int32_t)ignoring, (int32_t)ignore_index, (int32_t)mean,
+                   one_cluster ? loss : nullptr);
   if (st != LMHEAD_OK || each || one_cluster) return st;
   return launch_head(lmh::xent_reduce_kernel, 1, 1024, 0, stream, 1u, (const float*)row_loss,
-                     (int32_t)rows, (const int32_t*)k.n_rows, (int32_t)mean, loss);
+                     targets, (int32_t)rows, (int32_t)ignoring, (int32_t)ignore_index,
+                     (int32_t)mean, loss);
 }
 
 int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, const void* W,

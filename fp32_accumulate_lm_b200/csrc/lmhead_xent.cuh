@@ -1274,7 +1274,8 @@ __device__ __forceinline__ float xent_target_logit(const uint4* __restrict__ h,
 // others' (m, s):
 //   lse - z_t = log1p(s * 2^(m - x_t))                        where the target leads,
 //             = (m - x_t + log2(s + 2^(x_t - m))) / log2(e)   elsewhere,
-// so the loss of a row that is almost sure of its target keeps its bits. Ignored rows get 0 and 0;
+// so the loss of a row that is almost sure of its target keeps its bits. Ignored rows get 0 and 0 (they
+// have no place among the packed rows; where rows were not packed, their target is `ignore`);
 // a target outside [0, V) makes the row's loss NaN, and its lse is that of all entries. Where the
 // launch is a single cluster (at most 64 rows), its first block also adds the rows up in order
 // (`total`), which saves the next launch.
@@ -1293,11 +1294,12 @@ __global__ void __launch_bounds__(1024)
                      const int32_t* __restrict__ targets, const uint4* __restrict__ hidden,
                      const uint4* __restrict__ W, int32_t row_vecs,
                      const uint16_t* __restrict__ bias, float alpha, float z_loss,
-                     float* row_loss, float* lse_out, const int32_t* __restrict__ n_rows,
+                     float* row_loss, float* lse_out, int32_t ignoring, int32_t ignore,
                      int32_t mean, float* total) {
   constexpr int kOwn = kFoldSegs * kRows / 1024;  // segments of a lane
   __shared__ float2 seg[kFoldSegs][kRows + 1];
   __shared__ float s_loss[kRows];
+  __shared__ int32_t s_counts[kRows];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1327,7 +1329,7 @@ __global__ void __launch_bounds__(1024)
   const int32_t r = r0 + warp;
   const bool mine = warp < kRows && r < rows;  // the whole warp
   const int32_t t = mine ? targets[r] : -1;
-  const bool counts = mine && (place == nullptr || place[r] >= 0);
+  const bool counts = mine && !(ignoring && t == ignore);
   const bool held = counts && t >= 0 && t < V;
   float zt = 0.0f;
   if (held)
@@ -1371,14 +1373,22 @@ __global__ void __launch_bounds__(1024)
     row_loss[r] = loss;
   }
   if (total == nullptr) return;
-  if (warp < kRows && lane == 0) s_loss[warp] = loss;
+  if (warp < kRows && lane == 0) {
+    s_loss[warp] = loss;
+    s_counts[warp] = counts;
+  }
   cluster_sync_all();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     float sum = 0.0f;
-    for (uint32_t c = 0; c < gridDim.x; ++c)
+    int32_t n = 0;
+    for (uint32_t c = 0; c < gridDim.x; ++c) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) sum += cluster_load_f32(&s_loss[i], c);
-    *total = mean ? sum / (float)max(n_rows != nullptr ? *n_rows : rows, 1) : sum;
+      for (int i = 0; i < kRows; ++i) {
+        sum += cluster_load_f32(&s_loss[i], c);
+        n += cluster_load(&s_counts[i], c);
+      }
+    }
+    *total = mean ? sum / (float)max(n, 1) : sum;
   }
   cluster_sync_all();  // (the other blocks' sums have been read)
 }
@@ -1386,25 +1396,33 @@ __global__ void __launch_bounds__(1024)
 // The rows' losses added in a fixed order (each of 1024 threads every 1024th row, then a tree),
 // and divided by the number of rows that count (at least 1) for the mean.
 __global__ void __launch_bounds__(1024)
-    xent_reduce_kernel(const float* __restrict__ row_loss, int32_t rows,
-                       const int32_t* __restrict__ n_rows, int32_t mean, float* loss) {
+    xent_reduce_kernel(const float* __restrict__ row_loss, const int32_t* __restrict__ targets,
+                       int32_t rows, int32_t ignoring, int32_t ignore, int32_t mean, float* loss) {
   __shared__ float part[32];
+  __shared__ int32_t count[32];
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float s = 0.0f;
-  for (int32_t r = threadIdx.x; r < rows; r += 1024) s += row_loss[r];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  s = part[threadIdx.x];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (threadIdx.x == 0) {
-    const int32_t n = n_rows != nullptr ? *n_rows : rows;
-    *loss = mean ? s / (float)max(n, 1) : s;
+  int32_t n = 0;
+  for (int32_t r = threadIdx.x; r < rows; r += 1024) {
+    s += row_loss[r];
+    n += !(ignoring && targets[r] == ignore);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) {
+    part[warp] = s;
+    count[warp] = n;
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  s = part[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  n = __reduce_add_sync(0xffffffffu, count[lane]);
+  if (lane == 0) *loss = mean ? s / (float)max(n, 1) : s;
 }
 
 // ------------------------------------------------------------------ factors of the gradient

@@ -12,6 +12,7 @@ less than H 2^-24 of the sum of their sizes; 1e-4 is the bound the head's own te
     scale * (u + 2 dz_r + 2^-20) * (|d| @ |W|) (or (|d|^T @ |h|)), where |d| counts the softmax term
     and the target's 1 apart, plus the fp32 sums (1e-4 of the same, as above, at most (K) 2^-23),
     plus the final rounding, u of the value, and half the smallest subnormal;
+  * a softmax value below 2^-126 may be 0 (fp32's normal range): 2^-126 of the factor;
   * with fp16 an entry below 2^-14 of the scaled range is off by half a subnormal step instead:
     2^-25 of a range whose largest factor is at least 2^13: 2^-38 of that factor.
 """
@@ -84,7 +85,7 @@ class CrossEntropy:
         p = torch.exp(z - lse[:, None])
         d = a * p
         d[torch.arange(n, device=dev), t] -= g
-        off = (p * a.abs()) * (u + 2 * dz[:, None] + 2.0 ** -20)
+        off = (p * a.abs()) * (u + 2 * dz[:, None] + 2.0 ** -20) + a.abs() * 2.0 ** -126
         off[torch.arange(n, device=dev), t] += g.abs() * (u + 2.0 ** -22)
         if dtype == torch.float16 and n:
             top = torch.maximum(a.abs().max(), g.abs().max()) if reduction == "none" else a.abs().max()
