@@ -40,10 +40,10 @@
 // and what they hold (NaN of padding) never meets a product. The number of rows that count is known
 // on the device only; the tile walk reads it there.
 //
-// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue, warp 10 tile scheduler (cluster launch
-// control, in launch order); with big tiles warps 10-17 are epilogue warps too and the scheduler is
-// warp 18. Results are the same on every run: no split's order varies, an element of dH is added to
-// once a launch, and the only atomics are minima of row numbers.
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 and 10-17 the epilogue of one accumulator and of the
+// other, warp 18 tile scheduler (cluster launch control, in launch order). Results are the same on
+// every run: no split's order varies, an element of dH is added to once a launch, and the only
+// atomics are minima of row numbers.
 #pragma once
 
 #include "lmhead_bf16.cuh"
@@ -80,10 +80,12 @@ struct XentTile {
   static constexpr int kBBytes = kBRows * 64 * 2;
   static constexpr int kStageBytes = kABytes + kBBytes + (kBig ? kABytes : 0);  // (A and B alike)
   static constexpr int kStages = kShape == kXPair ? 6 : 4;    // 192 KB each way
-  // A big tile's accumulators have 8 epilogue warps each: TMEM is full, so the tensor pipe waits
-  // for whichever is read out last (with 8 warps for both in turn, the logits of 4096 x 1024 x
-  // 50304 took 371 us and not 356).
-  static constexpr int kEpiWarps = kBig ? 2 * kXEpiWarps : kXEpiWarps;
+  // Each accumulator has 8 epilogue warps of its own. A big tile fills TMEM, so the tensor pipe waits
+  // for whichever accumulator is read out last (with 8 warps for both in turn, the logits of 4096 x
+  // 1024 x 50304 took 371 us and not 356); and tiles of few K steps are bound by the epilogue, where the
+  // loads and stores of two tiles overlap (the weight gradient of 96 x 2048 x 151936: 324 us with 8
+  // warps in all, 304 so).
+  static constexpr int kEpiWarps = 2 * kXEpiWarps;
   static constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
   static constexpr size_t kSmem =
       1024 + (size_t)kStages * kStageBytes + kEpiWarps * kXStoreBox + 512;
@@ -1096,7 +1098,8 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;      // TMEM lanes this warp may access
-    const int half = ((warp - 2) >> 2) & 1;  // which 128 of the accumulator's columns
+    const int group = (warp - 2) / kXEpiWarps;  // its accumulator
+    const int half = ((warp - 2) >> 2) & 1;     // which 128 of the accumulator's columns
     const XentStage st{smem_u32(staging + (warp - 2) * kXStoreBox)};
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1109,8 +1112,12 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (tc.prob == -2) break;
       if (tc.prob < 0) continue;
       const XentProblem& q = p.prob[tc.prob];
-      // this warp's accumulator: its own of a big tile's two, else the one whose turn it is
-      const int h = kBig ? (warp - 2) / kXEpiWarps : acc;
+      // the tile's accumulator (a big tile has both), and this warp's
+      const int h = kBig ? group : acc;
+      const uint32_t tile_phase = acc_phase;
+      if (!kBig) acc ^= 1;
+      if (kBig || acc == 0) acc_phase ^= 1u;
+      if (h != group) continue;
       // The rows and columns of its part of the accumulator. A big tile's accumulators are the
       // halves of each CTA's A rows, or of its B rows: 128 columns of either CTA's.
       int32_t row0 = tc.m0 + quarter * 32, col = tc.n0 + half * kXChunk;
@@ -1124,7 +1131,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (!kBig && q.kind == kXentStats && row < n_rows) target = p.targets[row];
       if (q.kind == kXentDlogits && row < n_rows) info = p.row_info[row];
       if (q.kind == kXentDweight && row < q.m_len) first = p.first[q.out_off + row];
-      if (!wait_bounded(tfull0 + 8 * h, acc_phase, p.wait, abort_flag, kSleepHintNs)) {
+      if (!wait_bounded(tfull0 + 8 * h, tile_phase, p.wait, abort_flag, kSleepHintNs)) {
         fail(kRoleEpilogue, abort_flag);
         break;
       }
@@ -1145,8 +1152,6 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
         mbar_arrive_remote(tempty0 + 8 * h, 0);
       else
         mbar_arrive(tempty0 + 8 * h);
-      if (!kBig) acc ^= 1;
-      if (kBig || acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_all();  // the stores have left this CTA's shared memory and landed
     __syncwarp();
