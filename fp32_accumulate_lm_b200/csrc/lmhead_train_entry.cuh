@@ -85,14 +85,30 @@ XentForward carve_forward(Carver& c, int64_t rows, int64_t H, int64_t V, bool ig
 // The vocabulary in pieces of `piece` entries (a multiple of the tile width): d of a piece, 16 bits
 // a row and entry, takes about 128 MB, near what L2 holds, but a piece has at least 4096 entries,
 // so that its products fill the device at any number of rows. Pieces of equal length.
-// The splits of dH's K (a piece) make that product's tiles as many as the device has units, and no
-// more (a second round costs a whole tile's time), at 512 entries a split or more; each split has an
-// fp32 buffer of its own, and they are added in order at the end. (dH of 96 x 2048 x 151936: 259 us
-// with 18 splits of 8 tiles on 148 SMs, 287 with 19.)
+// `splits` is the most that dH's K (a piece) is split into, for which there are buffers.
 struct XentPieces {
   int64_t rows_pad, piece;
   int32_t n_pieces, splits;
 };
+
+// How many parts dH's K (a piece) is split into, at 512 entries a part or more; each has an fp32
+// buffer of its own, and they are added in order at the end. For dH alone its tiles are as many as
+// the device has units, and no more, as a second round costs a whole tile's time (96 x 2048 x
+// 151936: 259 us with 18 splits of 8 tiles on 148 SMs, 287 with 19). Beside dW they leave units to
+// dW's tiles, so that the one reads W while the other writes: 2/5 of the units for lone CTAs, where
+// memory bounds both (both gradients of 8 x 1024 x 50304: 108 us with 14 splits, 127 with 32; of 32
+// x 1024 x 32768: 74 and 100), and 2/3 for pairs (1000 x 1024 x 32768: 205 us with 3, 209 with 4;
+// with 2, as much as with 4).
+int32_t xent_splits(const XentPieces& x, int64_t rows, int64_t H, bool beside) {
+  const bool pair = rows > 128;
+  const int64_t units = pair ? (beside ? 49 : 74) : (beside ? 59 : 148);
+  const int64_t tiles = (pair ? x.rows_pad / 256 : 1) * ((H + lmh::kXN - 1) / lmh::kXN);
+  int64_t s = units / tiles;
+  const int64_t by_k = x.piece / 512;
+  if (s > by_k) s = by_k;
+  if (s > 32) s = 32;
+  return (int32_t)(s < 1 ? 1 : s);
+}
 
 XentPieces xent_pieces(int64_t rows, int64_t H, int64_t V) {
   XentPieces x;
@@ -103,15 +119,7 @@ XentPieces xent_pieces(int64_t rows, int64_t H, int64_t V) {
   x.n_pieces = (int32_t)((v_pad + most - 1) / most);
   x.piece = round_up((v_pad + x.n_pieces - 1) / x.n_pieces, lmh::kXN);
   x.n_pieces = (int32_t)((V + x.piece - 1) / x.piece);
-  const bool pair = rows > 128;
-  const int64_t units = pair ? 74 : 148;
-  const int64_t tiles =
-      (pair ? x.rows_pad / 256 : 1) * ((H + lmh::kXN - 1) / lmh::kXN);
-  int64_t s = units / tiles;
-  const int64_t by_k = x.piece / 512;
-  if (s > by_k) s = by_k;
-  if (s > 32) s = 32;
-  x.splits = (int32_t)(s < 1 ? 1 : s);
+  x.splits = xent_splits(x, rows, H, false);
   return x;
 }
 
@@ -350,6 +358,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   const bool ignoring = ignore_index != LMHEAD_IGNORE_NONE;
   const bool fp16 = dtype == LMHEAD_DTYPE_F16;
   const XentShape shape = xent_shape(dev, rows, V, true);
+  const int32_t splits = xent_splits(x, rows, H, d_W != nullptr);
   const XentPack& k = b.pack;
   if (ignoring) {
     st = launch_pack(k, hidden, targets, rows, H, ignore_index, stream);
@@ -391,7 +400,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   }
   if (st == LMHEAD_OK && d_hidden != nullptr)
     st = encode_2d(&maps.m[lmh::kMapDh], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, b.dh_partial, H,
-                   (int64_t)x.splits * x.rows_pad, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+                   (int64_t)splits * x.rows_pad, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (st == LMHEAD_OK && d_W != nullptr) st = encode_xent_store(&maps.m[lmh::kMapDw], d_W, H, V);
   if (st != LMHEAD_OK) return st;
 
@@ -448,7 +457,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
       q.b_flat = flat;
       q.b_off = (int32_t)start(c);
       q.b_k = 1;
-      q.splits = x.splits;
+      q.splits = splits;
       q.add = c > 0;
       p.prob[p.n_problems++] = q;
     }
@@ -478,7 +487,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   f.packed_targets = p.targets;
   f.lost = b.lost;
   f.scale = b.scale;
-  f.splits = x.splits;
+  f.splits = splits;
   f.split_len = x.rows_pad * H;
   f.partial = b.dh_partial;
   f.W = reinterpret_cast<const uint4*>(W);

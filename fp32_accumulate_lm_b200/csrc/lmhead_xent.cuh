@@ -754,7 +754,8 @@ __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const Xent
 __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t split,
-                                                 int32_t row0, int32_t col) {
+                                                 int32_t row0, int32_t n_rows, int32_t col) {
+  if (row0 >= n_rows) return;  // the whole warp
   const CUtensorMap* map = &maps.m[kMapDh];
   const int32_t y = split * p.rows_pad + row0;
   xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
@@ -1146,7 +1147,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       else if (q.kind == kXentDweight)
         xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col);
       else
-        xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, col);
+        xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, n_rows, col);
       tc_fence_before_sync();
       if constexpr (kPair)
         mbar_arrive_remote(tempty0 + 8 * h, 0);
@@ -1584,7 +1585,7 @@ __device__ __forceinline__ void xent_finish_hidden(const XentFinishParams& p) {
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     const float4* src =
         reinterpret_cast<const float4*>(p.partial) + ((int64_t)at * row_vecs + x) * 2;
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t k = 0; k < p.splits; ++k) xent_add8(s, src + k * (p.split_len / 4));
     const int32_t t = p.targets[r];
     if (t >= 0 && t < p.V)  // (elsewhere the row is NaN already)

@@ -304,7 +304,8 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * step of that type, fp16 with a common power of two taken out); every sum is fp32.
  *
  * Both are deterministic. The loss and lse of a row do not depend on the other rows of the call, bit
- * for bit; the gradients' sums run over the rows that count in order. The target's logit is summed in
+ * for bit; the gradients' sums run over the rows that count in order, and d_hidden's over parts of the
+ * vocabulary, of which there are fewer where d_W is asked for with it. The target's logit is summed in
  * fp32 outside the tensor cores, whose accumulator truncates; so losses are not the negatives of
  * lmhead_logprobs_f32's results to the last bit, but closer to the exact ones.
  *
