@@ -377,20 +377,18 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
                    (int32_t)(reduction == LMHEAD_REDUCE_MEAN), z_loss, alpha, b.row_info, b.lost, b.scale, b.first);
   if (st != LMHEAD_OK) return st;
 
-  // the forms of hidden and W as B's MN-major operand: in 3-D boxes, or where H is no multiple of
-  // 64, in 2-D ones of 64 x 64
-  const bool flat = H % 64 != 0;
   const void* h = ignoring ? k.hidden : hidden;
   const int64_t h_rows = ignoring ? round_up(rows, lmh::kBK) : rows;
   lmh::XentMaps maps = {};
   st = encode_xent(&maps.m[lmh::kMapHidden], h, H, h_rows, shape.wide_a());
   if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
-  if (st == LMHEAD_OK)
-    st = flat ? encode_xent(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, 64)
-              : encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, shape.tall_b() / 64);
-  if (st == LMHEAD_OK)
-    st = flat ? encode_xent(&maps.m[lmh::kMapWMn], W, H, V, 64)
-              : encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, shape.wide_b() / 64);
+  // hidden and W as B's MN-major operand (below 64 columns every tile is an edge)
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapHiddenEdge], h, H, h_rows, 64);
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapWEdge], W, H, V, 64);
+  if (st == LMHEAD_OK && H >= 64)
+    st = encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, shape.tall_b() / 64);
+  if (st == LMHEAD_OK && H >= 64)
+    st = encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, shape.wide_b() / 64);
   for (int i = 0; i < (x.n_pieces > 1 ? 2 : 1) && st == LMHEAD_OK; ++i) {
     st = encode_xent(&maps.m[lmh::kMapD + i], b.d[i], x.piece, x.rows_pad, shape.wide_a());
     if (st == LMHEAD_OK)
@@ -454,7 +452,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
                                          lmh::kMapWMn, H, length(c));
       q.m_rows = 1;
       q.b_mn = 1;
-      q.b_flat = flat;
+      q.b_edge = lmh::kMapWEdge;
       q.b_off = (int32_t)start(c);
       q.b_k = 1;
       q.splits = splits;
@@ -467,7 +465,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
       q.m_len = (int32_t)length(c);
       q.k_rows = 1;
       q.a_mn = q.b_mn = 1;
-      q.b_flat = flat;
+      q.b_edge = lmh::kMapHiddenEdge;
       q.out_off = (int32_t)start(c);
       q.out_map = lmh::kMapDw;
       q.add = accumulate != 0;

@@ -106,8 +106,8 @@ enum : int32_t {
 // a 3-D view [columns / 64][rows][64], a box being 64 rows of every 64-column block of the CTA's
 // tile. One box a stage and operand either way: with 64 x 64 boxes, two to four of them, the same
 // loads fed the tensor cores at 1150 TFLOP/s and not at 1325 (4096 x 4096 x 128256 logits under
-// the power cap). Where H is no multiple of 64 the 3-D view of hidden and W does not exist, and
-// their MN-major tiles come as 64 x 64 boxes of the 2-D matrix.
+// the power cap). The view of hidden and W has the whole blocks of H only; a tile at the edge of H
+// takes its columns as 64 x 64 boxes of the 2-D matrix, as many as it needs.
 enum : int32_t {
   kMapHidden = 0,    // [rows, H], K-major
   kMapHiddenMn = 1,  // [rows, H], MN-major
@@ -118,7 +118,9 @@ enum : int32_t {
   kMapDStore = 8,    // the same in boxes of 32 rows of 32 columns, 64-byte swizzle (stores)
   kMapDw = 10,       // dW [V, H] in the same boxes (stores)
   kMapDh = 11,       // the fp32 sums of dH [splits * rows_pad, H], boxes of 32 rows of 16 columns
-  kMapCount = 12,
+  kMapHiddenEdge = 12,  // hidden and W in boxes of 64 x 64
+  kMapWEdge = 13,
+  kMapCount = 14,
 };
 struct XentMaps {
   CUtensorMap m[kMapCount];
@@ -127,8 +129,8 @@ struct XentMaps {
 struct XentProblem {
   int32_t kind;
   int32_t a_map, b_map, out_map;
+  int32_t b_edge;         // an MN-major B's map for tiles at the edge of H
   int32_t a_mn, b_mn;     // 1: the operand is MN-major (its K runs down the rows of its matrix)
-  int32_t b_flat;         // 1: an MN-major B comes as 2-D boxes
   int32_t m_rows;         // 1: M is the number of rows that count (else m_len)
   int32_t k_rows;         // 1: K is the number of rows that count (else k_len)
   int32_t m_len, n_len, k_len;
@@ -378,6 +380,24 @@ struct XentTileAt {
 };
 
 __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
+
+// Half the columns of a tile, a multiple of 64 (lone: 32): what either CTA of a pair loads of B, and
+// what either half of the epilogue's warps takes. All of them but at the edge of H, where the tile
+// is as narrow as what is left, since its MMAs cost by the column (both gradients of 700 x 1032 x
+// 32771, with 8 columns in a row's fifth tile: 202 us, with whole tiles 207; 1000 x 896 x 65536: 350
+// and 357). Vocab entries are many, and their last tile stays whole.
+template <int kShape>
+__device__ __forceinline__ int32_t xent_share(const XentProblem& q, int32_t n0) {
+  using T = XentTile<kShape>;
+  const int32_t all = T::cols(q.wide) / 2, unit = T::kPair ? 64 : 32;
+  if (q.kind < kXentDweight) return all;
+  return min(all, ceil_div(q.n_len - n0, 2 * unit) * unit);
+}
+// The part of it that is accumulator h's. (A big wide tile's accumulators share its columns.)
+template <int kShape>
+__device__ __forceinline__ int32_t xent_share_of(const XentProblem& q, int32_t share, int h) {
+  return XentTile<kShape>::kBig && q.wide ? min(max(share - h * kXChunk, 0), kXChunk) : share;
+}
 
 // The launch's tiles: the problems one after another, each split by split, M tiles in groups of the
 // problem's own number, N-major within a group. What does not depend on the tile is worked out once:
@@ -709,11 +729,12 @@ template <bool kF16>
 __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t first,
-                                                 int32_t row0, int32_t row, int32_t col) {
+                                                 int32_t row0, int32_t row, int32_t col,
+                                                 int32_t cols) {
   const float scale = zero ? 0.0f : p.scale[1];  // (no row counts: 0, whatever the scale is)
   const bool add_row = q.add && row < q.m_len;
   const int64_t at = (int64_t)(q.out_off + row) * p.H;
-  xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
+  xent_columns(tacc, zero, min(cols, p.H - col), [&](int c, uint32_t(&r)[32]) {
     const int32_t x = col + c;
 #pragma unroll
     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
@@ -754,11 +775,12 @@ __device__ __forceinline__ void xent_epi_dweight(const XentParams& p, const Xent
 __device__ __forceinline__ void xent_epi_dhidden(const XentParams& p, const XentProblem& q,
                                                  const XentMaps& maps, const XentStage& st,
                                                  uint32_t tacc, bool zero, int32_t split,
-                                                 int32_t row0, int32_t n_rows, int32_t col) {
+                                                 int32_t row0, int32_t n_rows, int32_t col,
+                                                 int32_t cols) {
   if (row0 >= n_rows) return;  // the whole warp
   const CUtensorMap* map = &maps.m[kMapDh];
   const int32_t y = split * p.rows_pad + row0;
-  xent_columns(tacc, zero, p.H - col, [&](int c, uint32_t(&r)[32]) {
+  xent_columns(tacc, zero, min(cols, p.H - col), [&](int c, uint32_t(&r)[32]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (col + c + 16 * k >= p.H) break;
@@ -875,17 +897,18 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       }
       const XentProblem& q = p.prob[tc.prob];
       const CUtensorMap* ma = &maps.m[q.a_map];
-      const CUtensorMap* mb = &maps.m[q.b_map];
+      const bool edge = q.b_mn && tc.n0 + T::cols(q.wide) > q.n_len;
+      const CUtensorMap* mb = &maps.m[edge ? q.b_edge : q.b_map];
       // this CTA's part of the tile: its half of the rows of A and of B in a pair
       const int32_t m0 = tc.m0 + (kPair ? (int32_t)rank * (T::rows(q.wide) / 2) : 0);
-      const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * (T::cols(q.wide) / 2) : 0) +
-                         (q.b_k ? 0 : q.b_off);
+      const int32_t share = xent_share<kShape>(q, tc.n0);
+      const int32_t n0 = tc.n0 + (kPair ? (int32_t)rank * share : 0) + (q.b_k ? 0 : q.b_off);
       const uint32_t a_bytes = (kBig && !q.wide ? 2u : 1u) * T::kABytes;
       // A K-major A box brings a_rows rows only; what lies below them in the tile is other rows' of
       // the accumulator, and nobody reads those.
-      const uint32_t tx = (kPair ? 2u : 1u) * T::kStageBytes -
+      const int b_blocks = (kPair ? share : 2 * share) / 64;
+      const uint32_t tx = (kPair ? 2u : 1u) * (a_bytes + (uint32_t)(b_blocks * kXBlock)) -
                           (kPair || q.a_mn ? 0u : (uint32_t)(128 - p.a_rows) * 128u);
-      const int b_blocks = (kBig && q.wide ? 2 : 1) * (T::kBRows / 64);
       for (int ks = 0; ks < tc.k_steps; ++ks) {
         if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, p.wait, abort_flag)) {
           fail(kRoleProducer, abort_flag);
@@ -906,7 +929,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
             xent_load_2d<kPair>(sa, ma, full, k, m0, pol);
           if (!q.b_mn) {
             xent_load_2d<kPair>(sb, mb, full, kb, n0, pol);
-          } else if (!q.b_flat) {
+          } else if (!edge) {
             xent_load_3d<kPair>(sb, mb, full, n0, kb, pol);
           } else {
             for (int i = 0; i < b_blocks; ++i)
@@ -938,7 +961,6 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    const uint32_t idesc0 = idesc_f16kind_f32(T::kM, kXN, !kF16);
     int stage = 0;
     uint32_t phase = 0;
     int acc = 0;
@@ -953,7 +975,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (tc.prob == -2) break;
       if (tc.prob < 0) continue;
       const XentProblem& q = p.prob[tc.prob];
-      const uint32_t idesc = idesc0 | ((uint32_t)q.a_mn << 15) | ((uint32_t)q.b_mn << 16);
+      const int32_t share = xent_share<kShape>(q, tc.n0);
       // one K = 16 step further along: 32 bytes in a K-major tile, 16 rows in an MN-major one
       const uint64_t a_step = q.a_mn ? (16 * 128) >> 4 : 32 >> 4;
       const uint64_t b_step = q.b_mn ? (16 * 128) >> 4 : 32 >> 4;
@@ -969,6 +991,10 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
         return true;
       };
       auto multiply = [&](int st, int h, bool more) {
+        const int32_t n = 2 * xent_share_of<kShape>(q, share, h);
+        if (n == 0) return;
+        const uint32_t idesc = idesc_f16kind_f32(T::kM, n, !kF16) | ((uint32_t)q.a_mn << 15) |
+                               ((uint32_t)q.b_mn << 16);
         const uint32_t sa = smem_u32(smem + (size_t)st * T::kStageBytes);
         const uint32_t sb = sa + (kBig && !q.wide ? 2u : 1u) * T::kABytes;
         // the second accumulator's part of the operand that a big tile has two of
@@ -1100,7 +1126,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;      // TMEM lanes this warp may access
     const int group = (warp - 2) / kXEpiWarps;  // its accumulator
-    const int half = ((warp - 2) >> 2) & 1;     // which 128 of the accumulator's columns
+    const int half = ((warp - 2) >> 2) & 1;     // which half of the accumulator's columns
     const XentStage st{smem_u32(staging + (warp - 2) * kXStoreBox)};
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1121,9 +1147,11 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (h != group) continue;
       // The rows and columns of its part of the accumulator. A big tile's accumulators are the
       // halves of each CTA's A rows, or of its B rows: 128 columns of either CTA's.
-      int32_t row0 = tc.m0 + quarter * 32, col = tc.n0 + half * kXChunk;
+      const int32_t share = xent_share<kShape>(q, tc.n0);
+      const int32_t cols = xent_share_of<kShape>(q, share, h);
+      int32_t row0 = tc.m0 + quarter * 32, col = tc.n0 + half * share;
       if (kPair) row0 += (int32_t)rank * (T::rows(q.wide) / 2);
-      if (kBig && q.wide) col += half * kXChunk + h * kXChunk;
+      if (kBig && q.wide) col += h * kXChunk;
       if (kBig && !q.wide) row0 += h * T::kRows;
       const int32_t row = row0 + lane;
       // what the row needs besides the sums, on its way during the wait
@@ -1139,15 +1167,15 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       tc_fence_after_sync();
       const bool zero = tc.k_steps == 0;
       const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                            (uint32_t)(h * kXN + half * kXChunk);
+                            (uint32_t)(h * kXN + half * cols);
       if (!kBig && q.kind == kXentStats)  // (the loss takes no big tiles)
         xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
       else if (q.kind == kXentDlogits)
         xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, n_rows, info, col);
       else if (q.kind == kXentDweight)
-        xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col);
+        xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col, cols);
       else
-        xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, n_rows, col);
+        xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, n_rows, col, cols);
       tc_fence_before_sync();
       if constexpr (kPair)
         mbar_arrive_remote(tempty0 + 8 * h, 0);

@@ -93,6 +93,22 @@ def test_splits_of_the_vocabulary(rows, H, V):
     compare(*run_both(*make(rows, H, V, "f16"), reduction="sum"))
 
 
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("H", [8, 48, 64, 128, 200, 248, 264, 320, 328, 384, 448, 504, 640, 1032])
+def test_edges_of_the_hidden_size(rows, H):
+    """The last tile of the gradients is as narrow as what is left of H, in steps of 64 columns (128
+    on a CTA pair), and takes its columns in boxes of their own."""
+    for V, dtype, masked in ((1500, "bf16", 0.2), (5001, "f16", 0.0)):
+        compare(*run_both(*make(rows, H, V, dtype, masked=masked, bias=True), reduction="sum"))
+
+
+@pytest.mark.parametrize("H", [40, 192, 320, 448, 520, 712, 960])
+def test_edges_of_big_tiles(H):
+    """As above in tiles of 512 columns, of which the second accumulator may have none."""
+    rows, V = 2048, 131072
+    compare(*run_both(*make(rows, H, V, "bf16", masked=0.3)))
+
+
 @pytest.mark.parametrize("rows,H,V,dtype", [(2100, 72, 130001, "bf16"), (4097, 64, 65537, "f16"),
                                             (16641, 136, 16200, "bf16"), (2048, 264, 131072, "f16")])
 def test_big_tiles(rows, H, V, dtype):
