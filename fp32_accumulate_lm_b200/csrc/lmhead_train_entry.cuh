@@ -51,10 +51,13 @@ struct XentPack {
   int32_t *targets = nullptr, *place = nullptr, *row_of = nullptr, *n_rows = nullptr;
 };
 
+// Entries from one packed row to the next.
+int64_t packed_cols(int64_t H) { return round_up(H, 64); }
+
 XentPack carve_pack(Carver& c, int64_t rows, int64_t H, bool ignoring) {
   XentPack k;
   if (!ignoring) return k;
-  k.hidden = c.take<uint4>(round_up(rows, lmh::kBK) * (H / 8));
+  k.hidden = c.take<uint4>(round_up(rows, lmh::kBK) * (packed_cols(H) / 8));
   k.targets = c.take<int32_t>(rows);
   k.place = c.take<int32_t>(rows);
   k.row_of = c.take<int32_t>(rows);
@@ -172,8 +175,8 @@ int launch_pack(const XentPack& k, const void* hidden, const int32_t* targets, i
   const unsigned blocks = (unsigned)((rows + block_rows - 1) / block_rows);
   return launch_head(lmh::xent_pack_kernel, blocks, lmh::kPackThreads, 0, stream, 1u,
                      reinterpret_cast<const uint4*>(hidden), targets, (int32_t)rows, block_rows,
-                     (int32_t)(H / 8), (int32_t)ignore_index, k.hidden, k.targets, k.place,
-                     k.row_of, k.n_rows);
+                     (int32_t)(H / 8), (int32_t)(packed_cols(H) / 8), (int32_t)ignore_index,
+                     k.hidden, k.targets, k.place, k.row_of, k.n_rows);
 }
 
 // A matrix of 16-bit elements in boxes of 64 columns by `box_rows` rows.
@@ -301,8 +304,9 @@ int run_xent_forward(const void* hidden, int dtype, int64_t rows, int64_t H, con
   }
   const XentShape shape = xent_shape(dev, rows, V, false);
   lmh::XentMaps maps = {};
-  st = encode_xent(&maps.m[lmh::kMapHidden], packing ? k.hidden : hidden, H,
-                   packing ? round_up(rows, lmh::kBK) : rows, shape.wide_a());
+  st = encode_xent(&maps.m[lmh::kMapHidden], packing ? k.hidden : hidden,
+                   packing ? packed_cols(H) : H, packing ? round_up(rows, lmh::kBK) : rows,
+                   shape.wide_a());
   if (st != LMHEAD_OK) return st;
   st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
   if (st != LMHEAD_OK) return st;
@@ -378,15 +382,16 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   if (st != LMHEAD_OK) return st;
 
   const void* h = ignoring ? k.hidden : hidden;
+  const int64_t h_cols = ignoring ? packed_cols(H) : H;
   const int64_t h_rows = ignoring ? round_up(rows, lmh::kBK) : rows;
   lmh::XentMaps maps = {};
-  st = encode_xent(&maps.m[lmh::kMapHidden], h, H, h_rows, shape.wide_a());
+  st = encode_xent(&maps.m[lmh::kMapHidden], h, h_cols, h_rows, shape.wide_a());
   if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapW], W, H, V, shape.wide_b());
   // hidden and W as B's MN-major operand (below 64 columns every tile is an edge)
-  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapHiddenEdge], h, H, h_rows, 64);
+  if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapHiddenEdge], h, h_cols, h_rows, 64);
   if (st == LMHEAD_OK) st = encode_xent(&maps.m[lmh::kMapWEdge], W, H, V, 64);
   if (st == LMHEAD_OK && H >= 64)
-    st = encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, H, h_rows, shape.tall_b() / 64);
+    st = encode_xent_mn(&maps.m[lmh::kMapHiddenMn], h, h_cols, h_rows, shape.tall_b() / 64);
   if (st == LMHEAD_OK && H >= 64)
     st = encode_xent_mn(&maps.m[lmh::kMapWMn], W, H, V, shape.wide_b() / 64);
   for (int i = 0; i < (x.n_pieces > 1 ? 2 : 1) && st == LMHEAD_OK; ++i) {
@@ -494,6 +499,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   f.side = b.side;
   f.side_bias = b.side_bias;
   f.hidden = reinterpret_cast<const uint4*>(h);
+  f.hidden_vecs = (int32_t)(h_cols / 8);
   f.d_weight = reinterpret_cast<uint4*>(d_W);
   f.d_bias = reinterpret_cast<uint16_t*>(d_bias);
   const int64_t hidden_blocks =
