@@ -40,8 +40,8 @@
 // and what they hold (NaN of padding) never meets a product. The number of rows that count is known
 // on the device only; the tile walk reads it there.
 //
-// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 and 10-17 the epilogue of one accumulator and of the
-// other, warp 18 tile scheduler (cluster launch control, in launch order). Results are the same on
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-9 epilogue (and 10-17, where each accumulator has its own),
+// the last warp tile scheduler (cluster launch control, in launch order). Results are the same on
 // every run: no split's order varies, an element of dH is added to once a launch, and the only
 // atomics are minima of row numbers.
 #pragma once
@@ -80,12 +80,14 @@ struct XentTile {
   static constexpr int kBBytes = kBRows * 64 * 2;
   static constexpr int kStageBytes = kABytes + kBBytes + (kBig ? kABytes : 0);  // (A and B alike)
   static constexpr int kStages = kShape == kXPair ? 6 : 4;    // 192 KB each way
-  // Each accumulator has 8 epilogue warps of its own. A big tile fills TMEM, so the tensor pipe waits
-  // for whichever accumulator is read out last (with 8 warps for both in turn, the logits of 4096 x
-  // 1024 x 50304 took 371 us and not 356); and tiles of few K steps are bound by the epilogue, where the
-  // loads and stores of two tiles overlap (the weight gradient of 96 x 2048 x 151936: 324 us with 8
-  // warps in all, 304 so).
-  static constexpr int kEpiWarps = 2 * kXEpiWarps;
+  // A big tile's accumulators have 8 epilogue warps each: TMEM is full, so the tensor pipe waits
+  // for whichever is read out last (with 8 warps for both in turn, the logits of 4096 x 1024 x
+  // 50304 took 371 us and not 356). So have those of lone CTAs, whose tiles of few K steps are bound
+  // by the epilogue: the loads and stores of two tiles overlap (the weight gradient of 96 x 2048 x
+  // 151936: 324 us with 8 warps in all, 304 so). Pairs have 8 for the tiles in turn: 16
+  // cost the loss of 4096 x 2048 x 151936 0 to 1.5 % and won 0 to 2 % for gradients of 300 to 1000 rows.
+  static constexpr bool kOwnWarps = kShape != kXPair;
+  static constexpr int kEpiWarps = kOwnWarps ? 2 * kXEpiWarps : kXEpiWarps;
   static constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
   static constexpr size_t kSmem =
       1024 + (size_t)kStages * kStageBytes + kEpiWarps * kXStoreBox + 512;
@@ -976,6 +978,11 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (tc.prob < 0) continue;
       const XentProblem& q = p.prob[tc.prob];
       const int32_t share = xent_share<kShape>(q, tc.n0);
+      const uint32_t layout = ((uint32_t)q.a_mn << 15) | ((uint32_t)q.b_mn << 16);
+      const uint32_t idesc[2] = {
+          layout | idesc_f16kind_f32(T::kM, 2 * xent_share_of<kShape>(q, share, 0), !kF16),
+          layout | idesc_f16kind_f32(T::kM, 2 * xent_share_of<kShape>(q, share, 1), !kF16)};
+      const bool empty = xent_share_of<kShape>(q, share, 1) == 0;  // (a big tile's second)
       // one K = 16 step further along: 32 bytes in a K-major tile, 16 rows in an MN-major one
       const uint64_t a_step = q.a_mn ? (16 * 128) >> 4 : 32 >> 4;
       const uint64_t b_step = q.b_mn ? (16 * 128) >> 4 : 32 >> 4;
@@ -991,10 +998,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
         return true;
       };
       auto multiply = [&](int st, int h, bool more) {
-        const int32_t n = 2 * xent_share_of<kShape>(q, share, h);
-        if (n == 0) return;
-        const uint32_t idesc = idesc_f16kind_f32(T::kM, n, !kF16) | ((uint32_t)q.a_mn << 15) |
-                               ((uint32_t)q.b_mn << 16);
+        if (kBig && h == 1 && empty) return;
         const uint32_t sa = smem_u32(smem + (size_t)st * T::kStageBytes);
         const uint32_t sb = sa + (kBig && !q.wide ? 2u : 1u) * T::kABytes;
         // the second accumulator's part of the operand that a big tile has two of
@@ -1002,8 +1006,8 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
         const uint32_t ob = kBig && q.wide ? (uint32_t)h * T::kBBytes : 0u;
         const uint64_t ad = q.a_mn ? sdesc_mnmajor_sw128(sa + oa) : sdesc_kmajor_sw128(sa + oa);
         const uint64_t bd = q.b_mn ? sdesc_mnmajor_sw128(sb + ob) : sdesc_kmajor_sw128(sb + ob);
-        mma4_f16_steps_elect<kPair>(tmem_base + (uint32_t)(h * kXN), ad, bd, a_step, b_step, idesc,
-                                    more);
+        mma4_f16_steps_elect<kPair>(tmem_base + (uint32_t)(h * kXN), ad, bd, a_step, b_step,
+                                    idesc[kBig ? h : 0], more);
       };
       auto release = [&](uint32_t bar) {
         if constexpr (kPair)
@@ -1125,7 +1129,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quarter = warp & 3;      // TMEM lanes this warp may access
-    const int group = (warp - 2) / kXEpiWarps;  // its accumulator
+    const int own = (warp - 2) / kXEpiWarps;    // its accumulator (kOwnWarps)
     const int half = ((warp - 2) >> 2) & 1;     // which half of the accumulator's columns
     const XentStage st{smem_u32(staging + (warp - 2) * kXStoreBox)};
     int acc = 0;
@@ -1140,11 +1144,11 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       if (tc.prob < 0) continue;
       const XentProblem& q = p.prob[tc.prob];
       // the tile's accumulator (a big tile has both), and this warp's
-      const int h = kBig ? group : acc;
+      const int h = kBig ? own : acc;
       const uint32_t tile_phase = acc_phase;
       if (!kBig) acc ^= 1;
       if (kBig || acc == 0) acc_phase ^= 1u;
-      if (h != group) continue;
+      if (T::kOwnWarps && h != own) continue;
       // The rows and columns of its part of the accumulator. A big tile's accumulators are the
       // halves of each CTA's A rows, or of its B rows: 128 columns of either CTA's.
       const int32_t share = xent_share<kShape>(q, tc.n0);
