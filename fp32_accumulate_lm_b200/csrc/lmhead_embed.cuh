@@ -32,8 +32,8 @@ namespace lmh {
 constexpr int kEmbedVecs = 128, kEmbedThreads = 256;
 template <bool kF16>
 __global__ void __launch_bounds__(kEmbedThreads)
-    embed_kernel(const int32_t* __restrict__ ids, int64_t tokens, int32_t v_begin, int32_t V,
-                 const uint4* __restrict__ W, int32_t row_vecs, int32_t pieces, float scale,
+    embed_kernel(const int32_t* ids, int64_t tokens, int32_t v_begin, int32_t V,
+                 const uint4* W, int32_t row_vecs, int32_t pieces, float scale,
                  uint4* out) {
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int32_t x = x0 + 32 * i;
-    q[i] = held && x < row_vecs ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+    q[i] = held && x < row_vecs ? src[x] : make_uint4(0u, 0u, 0u, 0u);
   }
   uint4* dst = out + t * row_vecs;
 #pragma unroll
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSor
     int32_t* to_keys = pass & 1 ? p.keys[1] : p.keys[0];
     int32_t* to_pos = pass & 1 ? p.pos[1] : p.pos[0];
     auto key_at = [&](int32_t i) {
-      if (pass > 0) return __ldcg(keys + i);
+      if (pass > 0) return load_cg(keys + i);
       const int64_t v = (int64_t)p.ids[i] - p.v_begin;
       return v >= 0 && v < p.V ? (int32_t)v : p.V;
     };
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSor
         const int32_t i = i0 + warp * (items * 32) + k * 32 + lane;
         const bool mine = k < items && i < end;
         key[k] = mine ? key_at(i) : -1;
-        from[k] = !mine ? 0 : pass > 0 ? __ldcg(pos + i) : i;
+        from[k] = !mine ? 0 : pass > 0 ? load_cg(pos + i) : i;
       }
     };
     auto place = [&]() {
@@ -274,7 +274,7 @@ __device__ __forceinline__ void embed_zero_rows(const EmbedSumParams& p, int32_t
   uint4* dst = reinterpret_cast<uint4*>(p.d_weight) + (int64_t)r0 * row_vecs;
   for (int32_t i = threadIdx.x; i < n * row_vecs; i += kSumThreads) {
     const int32_t r = r0 + i / row_vecs;
-    if (!((__ldg(p.seen + (r >> 5)) >> (r & 31)) & 1u)) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (!((p.seen[r >> 5] >> (r & 31)) & 1u)) dst[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const EmbedSumPa
     for (int i = 0; i < kSumBatch; ++i) {
       const int k = e + i;
       const bool used = k < n_all && s_key[k] < p.V;
-      q[i] = used ? __ldcs(reinterpret_cast<const uint2*>(src + (int64_t)s_pos[k] * p.H))
+      q[i] = used ? load_cs(reinterpret_cast<const uint2*>(src + (int64_t)s_pos[k] * p.H))
                   : make_uint2(0u, 0u);
       // what the row of a run that ends here holds, on its way with the rest
       old[i] = p.add && used && s_key[k + 1] != s_key[k] ? *embed_row(p, s_key[k], x)
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kJoinGroups* kSumThreads)
     const int32_t j1 = i + 1 + (int32_t)((int64_t)n * (group + 1) / kJoinGroups);
 #pragma unroll 8
     for (int32_t j = j0; j < j1; ++j) {
-      const float4 q = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)j * 2 * p.H));
+      const float4 q = load_cs(reinterpret_cast<const float4*>(src + (int64_t)j * 2 * p.H));
       a[0] += q.x;
       a[1] += q.y;
       a[2] += q.z;

@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
 // rows 2000 bytes apart 1370; loss: 415 and 474).
 constexpr int kPackRows = 32, kPackThreads = 256;
 __global__ void __launch_bounds__(kPackThreads)
-    xent_pack_kernel(const uint4* __restrict__ hidden, const int32_t* __restrict__ targets,
+    xent_pack_kernel(const uint4* hidden, const int32_t* targets,
                      int32_t rows, int32_t block_rows, int32_t row_vecs, int32_t packed_vecs,
                      int32_t ignore, uint4* packed,
                      int32_t* packed_targets, int32_t* place, int32_t* row_of, int32_t* n_rows) {
@@ -1268,7 +1268,7 @@ __global__ void __launch_bounds__(kPackThreads)
     const uint4* src = hidden + (int64_t)(r0 + i) * row_vecs;
     uint4* dst = packed + (int64_t)at * packed_vecs;
 #pragma unroll 4
-    for (int32_t x = lane; x < row_vecs; x += 32) dst[x] = __ldcs(src + x);
+    for (int32_t x = lane; x < row_vecs; x += 32) dst[x] = load_cs(src + x);
     if (row_vecs + lane < packed_vecs) dst[row_vecs + lane] = make_uint4(0u, 0u, 0u, 0u);
   }
   const int32_t end = (all + kBK - 1) / kBK * kBK;
@@ -1285,13 +1285,13 @@ __global__ void __launch_bounds__(kPackThreads)
 // rows of a mean. The loss is a difference against this one logit; for the others the same loss is
 // a factor of 1 + 1e-6 z in the softmax. Called by a whole warp, the result in every lane.
 template <bool kF16>
-__device__ __forceinline__ float xent_target_logit(const uint4* __restrict__ h,
-                                                   const uint4* __restrict__ w, int32_t row_vecs,
+__device__ __forceinline__ float xent_target_logit(const uint4* h,
+                                                   const uint4* w, int32_t row_vecs,
                                                    const uint16_t* bias, int32_t t, float alpha) {
   float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 4
   for (int32_t x = (int)(threadIdx.x & 31); x < row_vecs; x += 32) {
-    const uint4 a = __ldg(h + x), b = __ldg(w + x);
+    const uint4 a = h[x], b = w[x];
     const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1331,11 +1331,11 @@ __device__ __forceinline__ void xent_merge(float& m, float& s, float m2, float s
 constexpr int kFoldFew = 8, kFoldMany = 32, kFoldSegs = 128, kFoldCluster = 8;
 template <int kRows, bool kF16>
 __global__ void __launch_bounds__(1024)
-    xent_fold_kernel(const float2* __restrict__ partials, int32_t n_chunks, int32_t pitch,
-                     int32_t rows, int32_t V, const int32_t* __restrict__ place,
-                     const int32_t* __restrict__ targets, const uint4* __restrict__ hidden,
-                     const uint4* __restrict__ W, int32_t row_vecs,
-                     const uint16_t* __restrict__ bias, float alpha, float z_loss,
+    xent_fold_kernel(const float2* partials, int32_t n_chunks, int32_t pitch,
+                     int32_t rows, int32_t V, const int32_t* place,
+                     const int32_t* targets, const uint4* hidden,
+                     const uint4* W, int32_t row_vecs,
+                     const uint16_t* bias, float alpha, float z_loss,
                      float* row_loss, float* lse_out, int32_t ignoring, int32_t ignore,
                      int32_t mean, float* total) {
   constexpr int kOwn = kFoldSegs * kRows / 1024;  // segments of a lane
@@ -1359,7 +1359,7 @@ __global__ void __launch_bounds__(1024)
         float2 q[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          q[i] = c + i < c1 ? __ldcs(partials + (int64_t)(c + i) * pitch + at)
+          q[i] = c + i < c1 ? load_cs(partials + (int64_t)(c + i) * pitch + at)
                             : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) xent_merge(m, s, q[i].x, q[i].y);
@@ -1438,7 +1438,7 @@ __global__ void __launch_bounds__(1024)
 // The rows' losses added in a fixed order (each of 1024 threads every 1024th row, then a tree),
 // and divided by the number of rows that count (at least 1) for the mean.
 __global__ void __launch_bounds__(1024)
-    xent_reduce_kernel(const float* __restrict__ row_loss, const int32_t* __restrict__ targets,
+    xent_reduce_kernel(const float* row_loss, const int32_t* targets,
                        int32_t rows, int32_t ignoring, int32_t ignore, int32_t mean, float* loss) {
   __shared__ float part[32];
   __shared__ int32_t count[32];
@@ -1481,12 +1481,12 @@ __global__ void __launch_bounds__(1024)
 constexpr int kRowsBlock = 32;
 template <bool kF16>
 __global__ void __launch_bounds__(1024)
-    xent_rows_kernel(const float* __restrict__ lse, const int32_t* __restrict__ targets,
-                     const int32_t* __restrict__ row_of, int32_t rows,
-                     const int32_t* __restrict__ n_rows, int32_t V,
-                     const uint4* __restrict__ hidden, const uint4* __restrict__ W,
-                     int32_t row_vecs, const uint16_t* __restrict__ bias,
-                     const float* __restrict__ grad, int32_t per_row, int32_t mean, float z_loss,
+    xent_rows_kernel(const float* lse, const int32_t* targets,
+                     const int32_t* row_of, int32_t rows,
+                     const int32_t* n_rows, int32_t V,
+                     const uint4* hidden, const uint4* W,
+                     int32_t row_vecs, const uint16_t* bias,
+                     const float* grad, int32_t per_row, int32_t mean, float z_loss,
                      float alpha, float4* row_info, float* lost, float* scale, int32_t* first) {
   __shared__ float part[32];
   if (threadIdx.x == 0) pdl_trigger();
@@ -1592,7 +1592,7 @@ __device__ __forceinline__ void xent_fma8(float (&s)[8], float e, const uint4& q
 }
 
 __device__ __forceinline__ void xent_add8(float (&s)[8], const float4* src) {
-  const float4 u = __ldcs(src), v = __ldcs(src + 1);
+  const float4 u = load_cs(src), v = load_cs(src + 1);
   s[0] += u.x;
   s[1] += u.y;
   s[2] += u.z;
@@ -1626,7 +1626,7 @@ __device__ __forceinline__ void xent_finish_hidden(const XentFinishParams& p) {
     for (int32_t k = 0; k < p.splits; ++k) xent_add8(s, src + k * (p.split_len / 4));
     const int32_t t = p.targets[r];
     if (t >= 0 && t < p.V)  // (elsewhere the row is NaN already)
-      xent_fma8<kF16>(s, p.lost[at], __ldg(p.W + (int64_t)t * row_vecs + x));
+      xent_fma8<kF16>(s, p.lost[at], p.W[(int64_t)t * row_vecs + x]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] *= f;
     out = xent_pack8<kF16>(s);
@@ -1674,7 +1674,7 @@ __device__ __forceinline__ void xent_finish_weight(const XentFinishParams& p) {
         for (uint32_t bits = __shfl_sync(0xffffffffu, my, w); bits != 0; bits &= bits - 1) {
           const int32_t r = r0 + (w0 + w) * 32 + __ffs((int)bits) - 1;
           const float e = p.lost[r] * f;
-          if (mine) xent_fma8<kF16>(s, e, __ldg(p.hidden + (int64_t)r * p.hidden_vecs + x));
+          if (mine) xent_fma8<kF16>(s, e, p.hidden[(int64_t)r * p.hidden_vecs + x]);
           sb += e;
         }
       }
@@ -1703,9 +1703,9 @@ __global__ void __launch_bounds__(kFinishThreads)
 constexpr int kBiasCols = 64, kBiasParts = 8;
 template <bool kF16>
 __global__ void __launch_bounds__(kBiasCols* kBiasParts)
-    xent_bias_kernel(const float* __restrict__ part, int32_t pitch, int32_t cols, int32_t rows,
-                     const int32_t* __restrict__ n_rows, const float* __restrict__ scale,
-                     const int32_t* __restrict__ first, float* side, int32_t add,
+    xent_bias_kernel(const float* part, int32_t pitch, int32_t cols, int32_t rows,
+                     const int32_t* n_rows, const float* scale,
+                     const int32_t* first, float* side, int32_t add,
                      uint16_t* d_bias) {
   __shared__ float s_part[kBiasParts][kBiasCols];
   if (threadIdx.x == 0) pdl_trigger();

@@ -30,12 +30,49 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // stream start its on-chip set-up on the SMs it has already left (pdl_trigger at entry), and
 // itself touches global memory only after every earlier kernel of the stream has finished and
 // its writes are visible (pdl_wait, by every thread, after the set-up).
+// Behind the wait such a kernel loads coherently: no __ldg, and no const __restrict__ pointers that
+// allow the same. Those promise that the data does not change while the kernel is resident, but an
+// earlier kernel of the stream may still be writing it when this one's blocks start; a load that
+// made the promise could be moved above the wait, or answered by a cache that was filled before it.
+// Loads with a cache hint are the load_cs and load_cg below: volatile, so that they stay behind the
+// wait (and behind the cluster barriers) whatever the compiler knows of their addresses.
 
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Global loads of data that is read once (evicted first), and past the L1.
+__device__ __forceinline__ uint2 load_cs(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.cs.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_cs(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float2 load_cs(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.cs.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 load_cs(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t load_cg(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 
 // ------------------------------------------------------------------ mbarrier
 
