@@ -241,6 +241,14 @@ XentShape xent_shape(const DeviceInfo& dev, int64_t rows, int64_t V, bool gradie
   return {gradient && rows * V >= (int64_t)1 << 28 ? lmh::kXBig : lmh::kXPair, rows};
 }
 
+// Whether a shape's kernel has the epilogues of a launch's products. Big tiles have none for the
+// loss's statistics: its warps would leave their accumulators, and the loss, unwritten.
+bool xent_shape_serves(int shape, const lmh::XentParams& p) {
+  for (int i = 0; i < p.n_problems; ++i)
+    if (shape == lmh::kXBig && p.prob[i].kind == lmh::kXentStats) return false;
+  return true;
+}
+
 template <int kShape>
 int64_t xent_tiles(const lmh::XentParams& p) {
   using T = lmh::XentTile<kShape>;
@@ -257,6 +265,7 @@ template <int kShape>
 int launch_xent_shape(const DeviceInfo& dev, bool fp16, const lmh::XentMaps& maps,
                       const lmh::XentParams& p, lmhead_stream_t stream) {
   using T = lmh::XentTile<kShape>;
+  if (!xent_shape_serves(kShape, p)) return LMHEAD_ERR_SHAPE;
   const int64_t ctas = xent_tiles<kShape>(p) * (T::kPair ? 2 : 1);
   if (ctas > kInt32Max || (int64_t)T::kSmem > dev.smem_optin) return LMHEAD_ERR_SHAPE;
   return launch_head(
@@ -652,6 +661,17 @@ int run_embed_grad(const DeviceInfo& dev, const void* d_out, int dtype, const in
 }  // namespace
 
 extern "C" {
+
+#if LMHEAD_TEST_HOOKS
+// For the tests: the rule above for a launch with a product of `kind`. (No knob: it sets nothing.)
+int lmhead_debug_xent_shape_serves(int shape, int kind) {
+  lmh::XentParams p = {};
+  p.n_problems = 2;  // a product that every shape serves, then the one in question
+  p.prob[0].kind = lmh::kXentDweight;
+  p.prob[1].kind = kind;
+  return xent_shape_serves(shape, p) ? 1 : 0;
+}
+#endif
 
 size_t lmhead_cross_entropy_workspace_bytes(int64_t rows, int64_t H, int64_t V,
                                             int64_t ignore_index) {

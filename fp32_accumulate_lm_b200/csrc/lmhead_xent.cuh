@@ -1172,14 +1172,16 @@ __global__ void __launch_bounds__(XentTile<kShape>::kThreads, 1)
       const bool zero = tc.k_steps == 0;
       const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) +
                             (uint32_t)(h * kXN + half * cols);
-      if (!kBig && q.kind == kXentStats)  // (the loss takes no big tiles)
-        xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
-      else if (q.kind == kXentDlogits)
+      if (q.kind == kXentStats) {
+        if constexpr (!kBig)  // (big tiles are refused for the loss on the host)
+          xent_epi_stats<kF16>(p, q, tacc, zero, row, row < n_rows, target, col);
+      } else if (q.kind == kXentDlogits) {
         xent_epi_dlogits<kF16>(p, q, maps, st, tacc, zero, row0, row, n_rows, info, col);
-      else if (q.kind == kXentDweight)
+      } else if (q.kind == kXentDweight) {
         xent_epi_dweight<kF16>(p, q, maps, st, tacc, zero, first, row0, row, col, cols);
-      else
+      } else {
         xent_epi_dhidden(p, q, maps, st, tacc, zero, tc.split, row0, n_rows, col, cols);
+      }
       tc_fence_before_sync();
       if constexpr (kPair)
         mbar_arrive_remote(tempty0 + 8 * h, 0);
