@@ -131,7 +131,7 @@ struct XentBackward {
   float4* row_info;
   float *lost, *scale;
   int32_t* first;
-  float *side, *side_bias, *bias_part[2];
+  float *side, *bias_part[2];
   uint16_t* d[2];
   float* dh_partial;
 };
@@ -145,7 +145,6 @@ XentBackward carve_backward(Carver& c, const XentPieces& x, int64_t rows, int64_
   b.scale = c.take<float>(2);
   b.first = c.take<int32_t>(V);
   b.side = c.take<float>(rows * H);
-  b.side_bias = c.take<float>(rows);
   b.d[0] = c.take<uint16_t>(x.rows_pad * x.piece);
   for (int i = 0; i < 2; ++i) b.bias_part[i] = c.take<float>(x.rows_pad / 32 * x.piece);
   b.d[1] = x.n_pieces > 1 ? c.take<uint16_t>(x.rows_pad * x.piece) : b.d[0];
@@ -454,8 +453,7 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
                        lmh::kBiasCols * lmh::kBiasParts, 0, stream, 1u,
                        (const float*)b.bias_part[c & 1], (int32_t)x.piece,
                        (int32_t)length(c), (int32_t)rows, (const int32_t*)k.n_rows,
-                       (const float*)b.scale, (const int32_t*)(b.first + start(c)), b.side_bias,
-                       (int32_t)(accumulate != 0),
+                       (const float*)b.scale, (int32_t)(accumulate != 0),
                        reinterpret_cast<uint16_t*>(d_bias) + start(c));
       if (st != LMHEAD_OK) return st;
     }
@@ -506,16 +504,14 @@ int run_xent_backward(const void* hidden, int dtype, int64_t rows, int64_t H, co
   f.d_hidden = reinterpret_cast<uint4*>(d_hidden);
   f.first = b.first;
   f.side = b.side;
-  f.side_bias = b.side_bias;
   f.hidden = reinterpret_cast<const uint4*>(h);
   f.hidden_vecs = (int32_t)(h_cols / 8);
   f.d_weight = reinterpret_cast<uint4*>(d_W);
-  f.d_bias = reinterpret_cast<uint16_t*>(d_bias);
   const int64_t hidden_blocks =
       d_hidden == nullptr ? 0 : (rows * (H / 8) + lmh::kFinishThreads - 1) / lmh::kFinishThreads;
-  const int64_t slices =
-      d_W == nullptr ? 1 : (H / 8 + lmh::kFinishThreads - 1) / lmh::kFinishThreads;
-  const int64_t weight_blocks = d_W == nullptr && d_bias == nullptr ? 0 : rows * slices;
+  const int64_t slices = (H / 8 + lmh::kFinishThreads - 1) / lmh::kFinishThreads;
+  const int64_t weight_blocks = d_W == nullptr ? 0 : rows * slices;
+  if (hidden_blocks + weight_blocks == 0) return LMHEAD_OK;  // d_bias alone
   if (hidden_blocks + weight_blocks > kInt32Max) return LMHEAD_ERR_SHAPE;
   f.hidden_blocks = (int32_t)hidden_blocks;
   f.slices = (int32_t)slices;

@@ -159,7 +159,7 @@ struct XentParams {
   float2* partials;           // stats: [2 * ceil(V / 256)][rows]
   const float4* row_info;     // dlogits: (lse * log2(e), a, d at the target, target as int bits)
   const float* scale;         // device: [1] = the factor of the gradients
-  float* bias_part;           // dlogits: [rows_pad / 32][piece] column sums of d, or null
+  float* bias_part;           // dlogits: [rows_pad / 32][piece] column sums of d in fp32, or null
   int32_t piece;              // entries of a full piece (the pitch of bias_part)
   int32_t* first;             // [V]: the first row whose target is this entry (kXNoRow: none)
   float* side;                // [rows that count][H]: dW's row of that target before its rounding
@@ -631,28 +631,6 @@ struct XentStage {
       st_shared_v4(buf + row * 64u + (((uint32_t)j ^ ((row >> 1) & 3u)) << 4), w[4 * j],
                    w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
-  // The sums of the box's columns 2 * i and 2 * i + 1 over its 32 rows, in lanes i and i + 16: the
-  // even rows, then the odd rows, each in order.
-  template <bool kF16>
-  __device__ __forceinline__ float2 column_sums() const {
-    const uint32_t pair = threadIdx.x & 15, odd = (threadIdx.x >> 4) & 1;
-    __syncwarp();
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (uint32_t i = 0; i < 16; ++i) {
-      const uint32_t row = 2 * i + odd;
-      uint32_t w;
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(w)
-                   : "r"(buf + row * 64u + (((pair >> 2) ^ (i & 3u)) << 4) + (pair & 3u) * 4u)
-                   : "memory");
-      s.x += unpack16<kF16>(w & 0xffffu);
-      s.y += unpack16<kF16>(w >> 16);
-    }
-    s.x += __shfl_xor_sync(0xffffffffu, s.x, 16);
-    s.y += __shfl_xor_sync(0xffffffffu, s.y, 16);
-    return s;
-  }
   __device__ __forceinline__ void store(const CUtensorMap* map, int32_t x, int32_t y) const {
     fence_async_smem();
     __syncwarp();
@@ -668,6 +646,23 @@ __device__ __forceinline__ void xent_pack32(const uint32_t (&r)[32], uint32_t (&
 #pragma unroll
   for (int j = 0; j < 16; ++j)
     w[j] = pack16<kF16>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+}
+
+// The sums of 32 columns over the warp's 32 rows, a lane holding its row: lane c gets column c's.
+// Each step halves the columns that a lane holds and adds the other lane's half, so a column is a
+// tree of the rows, always the same one. `r` is used up.
+__device__ __forceinline__ float xent_column_sums(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + o]);
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, o);
+      r[j] = __float_as_uint((upper ? b : a) + other);
+    }
+  }
+  return __uint_as_float(r[0]);
 }
 
 // d of this thread's row over its 128 vocab entries of the piece, 16 bits, into the piece's buffer.
@@ -715,12 +710,9 @@ __device__ __forceinline__ void xent_epi_dlogits(const XentParams& p, const Xent
     uint32_t w[16];
     xent_pack32<kF16>(r, w);
     st.put(w);
-    if (p.bias_part != nullptr) {
-      const float2 sums = st.column_sums<kF16>();
-      float* at = p.bias_part + (int64_t)(row0 / 32) * p.piece + col + c;
-      if (lane < 16) reinterpret_cast<float2*>(at)[lane] = sums;
-    }
     st.store(&maps.m[q.out_map], col + c, row0);
+    if (p.bias_part != nullptr)  // of d in fp32: dbias needs no operand of a product
+      p.bias_part[(int64_t)(row0 / 32) * p.piece + col + c + lane] = xent_column_sums(r);
   });
 }
 
@@ -1551,10 +1543,10 @@ __global__ void __launch_bounds__(1024)
 // The launch that ends the gradient. Its first `hidden_blocks` blocks write dH from its partial
 // sums: the splits in order, plus what the target's entry of d lost in its rounding times the
 // target's row of W, times the factor, rounded once; ignored rows 0. A thread takes 8 entries of a
-// row. The other blocks write the rows of dW, and the entries of dbias, that are some row's target
-// once more, from the fp32 values that the products left in `side`: a block takes 2048 columns of
-// the target of one row that counts, if no earlier row has the same target, and adds what d lost
-// there, for all rows of that target in order. With it dH, dW and dbias are as far off as their own
+// row. The other blocks write the rows of dW that are some row's target once more, from the fp32
+// values that the product left in `side`: a block takes 2048 columns of the target of one row that
+// counts, if no earlier row has the same target, and adds what d lost there, for all rows of that
+// target in order. With it dH, dW and dbias are as far off as their own
 // rounding; without, by half as much again (96 weighted rows: 0.0026 and not 0.0017 of dH).
 struct XentFinishParams {
   int32_t rows, H, V;
@@ -1571,15 +1563,13 @@ struct XentFinishParams {
   const float* partial;
   const uint4* W;
   uint4* d_hidden;
-  // dW, dbias
+  // dW
   int32_t slices;                 // blocks a row
   const int32_t* first;
   const float* side;
-  const float* side_bias;
   const uint4* hidden;            // the rows that count
   int32_t hidden_vecs;            // from one to the next
-  uint4* d_weight;                // null: not wanted
-  uint16_t* d_bias;
+  uint4* d_weight;
 };
 constexpr int kFinishThreads = 256, kFinishScan = 16;
 
@@ -1648,13 +1638,11 @@ __device__ __forceinline__ void xent_finish_weight(const XentFinishParams& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t row_vecs = p.H / 8;
   const int32_t x = slice * kFinishThreads + (int)threadIdx.x;
-  const bool mine = p.d_weight != nullptr && x < row_vecs;
-  const bool bias = p.d_bias != nullptr && slice == 0 && threadIdx.x == 0;
+  const bool mine = x < row_vecs;
   const float f = p.scale[1];
   float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (mine)
     xent_add8(s, reinterpret_cast<const float4*>(p.side) + ((int64_t)i * row_vecs + x) * 2);
-  float sb = bias ? p.side_bias[i] : 0.0f;
   // the rows with this target, 4096 at a time (none is before row i)
   for (int32_t r0 = i & ~31; r0 < n; r0 += kFinishScan * kFinishThreads) {
     bool hit[kFinishScan];
@@ -1677,14 +1665,12 @@ __device__ __forceinline__ void xent_finish_weight(const XentFinishParams& p) {
           const int32_t r = r0 + (w0 + w) * 32 + __ffs((int)bits) - 1;
           const float e = p.lost[r] * f;
           if (mine) xent_fma8<kF16>(s, e, p.hidden[(int64_t)r * p.hidden_vecs + x]);
-          sb += e;
         }
       }
     }
     __syncthreads();
   }
   if (mine) p.d_weight[(int64_t)t * row_vecs + x] = xent_pack8<kF16>(s);
-  if (bias) p.d_bias[t] = (uint16_t)(pack16<kF16>(sb, 0.0f) & 0xffffu);
 }
 
 template <bool kF16>
@@ -1698,16 +1684,14 @@ __global__ void __launch_bounds__(kFinishThreads)
     xent_finish_weight<kF16>(p);
 }
 
-// dbias of a piece: the column sums that the product which made d left for each 32 rows, added in
-// fp32 (read again from d itself, 134 MB a piece of 4096 rows, this took 18 us a piece). A block
-// takes 64 columns, 8 threads each: every 8th block of 32 rows, then the eight in order. A target's
-// entry also goes to its first row's place in `side`, as in xent_epi_dweight.
+// dbias of a piece: the column sums of d in fp32 that the product which made d left for each 32
+// rows, added up (read again from d itself, 134 MB a piece of 4096 rows, this took 18 us a piece). A
+// block takes 64 columns, 8 threads each: every 8th block of 32 rows, then the eight in order.
 constexpr int kBiasCols = 64, kBiasParts = 8;
 template <bool kF16>
 __global__ void __launch_bounds__(kBiasCols* kBiasParts)
     xent_bias_kernel(const float* part, int32_t pitch, int32_t cols, int32_t rows,
-                     const int32_t* n_rows, const float* scale,
-                     const int32_t* first, float* side, int32_t add,
+                     const int32_t* n_rows, const float* scale, int32_t add,
                      uint16_t* d_bias) {
   __shared__ float s_part[kBiasParts][kBiasCols];
   if (threadIdx.x == 0) pdl_trigger();
@@ -1728,8 +1712,6 @@ __global__ void __launch_bounds__(kBiasCols* kBiasParts)
   t = n > 0 ? t * scale[1] : 0.0f;
   uint16_t* at = d_bias + c;
   if (add) t += unpack16<kF16>(*at);
-  const int32_t r = first[c];
-  if (r != kXNoRow) side[r] = t;
   *at = (uint16_t)(pack16<kF16>(t, 0.0f) & 0xffffu);
 }
 

@@ -301,7 +301,8 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * is always written. Any of the three may be NULL and is then not computed, but not all of them. A
  * row with a target outside [0, V) that is not ignored has NaN gradients, and so have d_W and
  * d_bias then. The products take dz in the operands' 16-bit type (each entry off by at most half a
- * step of that type, fp16 with a common power of two taken out); every sum is fp32.
+ * step of that type, fp16 with a common power of two taken out); every sum is fp32, and d_bias sums dz
+ * as it is before that rounding.
  *
  * Both are deterministic. The loss and lse of a row do not depend on the other rows of the call, bit
  * for bit; the gradients' sums run over the rows that count in order, and d_hidden's over parts of the
@@ -318,8 +319,8 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * A workspace serves one call at a time: not two that may run at once, as graphs or on streams.
  * rows == 0: the loss of REDUCE_SUM and REDUCE_MEAN is written as 0, and so are d_W and d_bias unless
  * they accumulate. Outputs and the workspace must not overlap each other or the inputs. The first
- * enqueues two to four kernels; the second three or four, and for each piece of the vocabulary one,
- * or two with d_bias. Each returns an lmhead_status.
+ * enqueues two to four kernels; the second three or four, and for each piece of the vocabulary one, or
+ * two with d_bias (two fewer in all for d_bias alone). Each returns an lmhead_status.
  */
 #define LMHEAD_IGNORE_NONE INT64_MIN
 typedef enum {
