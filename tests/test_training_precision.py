@@ -1,6 +1,7 @@
 """The precision of the training gradients where the elementwise bounds of tests/training_reference.py
-are too wide to tell: d_bias summed in fp32. The tests on the CPU show that the bounds tell the
-kernels' roundings from wrong ones."""
+are too wide to tell: the target's entry of d put back in fp32 (tests/training_precision.py derives
+the bounds), d_bias summed in fp32. The tests on the CPU show that the bounds tell the kernels'
+roundings from wrong ones."""
 import math
 
 import pytest
@@ -8,7 +9,7 @@ import torch
 
 import fp32_accumulate_lm_b200 as lm
 from gpu_helpers import check_status
-from training_precision import IGNORE, Centred, rounded
+from training_precision import IGNORE, Centred, assert_as_foretold, rounded
 from training_reference import assert_close, half_step
 
 DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
@@ -45,6 +46,71 @@ def make(device, rows, H, V, dtype="bf16", reduction="none", masked=0.0, targets
     return hidden.to(dt), W, t, bias, gl
 
 
+def gradients(hidden, W, t, b, gl, reduction, **kw):
+    loss, lse = lm.cross_entropy_f32(hidden, W, t, bias=b, reduction=reduction)
+    got = lm.cross_entropy_grad(hidden, W, t, lse, gl, bias=b, reduction=reduction, **kw)
+    check_status()
+    return got
+
+
+# ------------------------------------------------------------------ the target's entry of d
+
+CPU_SIZES = [(96, 64, 1500, "bf16", "none", "any"), (300, 64, 700, "f16", "none", "any"),
+             (1000, 64, 600, "bf16", "none", "twice"), (500, 64, 900, "bf16", "mean", "any")]
+
+
+@pytest.mark.parametrize("rows,H,V,dtype,reduction,targets", CPU_SIZES)
+def test_the_bounds_tell_a_missing_mend(rows, H, V, dtype, reduction, targets):
+    hidden, W, t, b, gl = make("cpu", rows, H, V, dtype, reduction, targets=targets)
+    c = Centred(hidden, W, t, bias=b, reduction=reduction, grad_loss=gl)
+    dt = DTYPES[dtype]
+
+    def outputs(mend):
+        got = c.outputs(c.round_d(mend))
+        return [rounded(x, dt) for x in got[:2]] + [rounded(c.d_bias(c.d), dt)]
+
+    assert_as_foretold(c, outputs("target"))
+    # a d that is off by what its logits may be rounds some entries the other way
+    c.d *= 1 + c.logits * (2 * torch.rand(c.d.shape, generator=torch.Generator().manual_seed(1)) - 1)
+    moved = outputs("target")
+    c = Centred(hidden, W, t, bias=b, reduction=reduction, grad_loss=gl)
+    assert_as_foretold(c, moved)
+    for wrong in ("nothing", "flipped") + (("first",) if targets == "twice" else ()):
+        for i in (0, 1):
+            if wrong == "first" and i == 0:
+                continue
+            got = [None] * 3
+            got[i] = outputs(wrong)[i]
+            with pytest.raises(AssertionError):
+                assert_as_foretold(c, got)
+
+
+CASES = [
+    (96, 64, 2000, "bf16", "none", 0.0, "any"),         # lone CTAs
+    (300, 64, 3000, "f16", "none", 0.3, "any"),         # pairs, masked rows
+    (700, 72, 9000, "bf16", "mean", 0.0, "any"),
+    (12000, 64, 7000, "bf16", "none", 0.0, "twice"),    # targets again 6000 rows later
+    (12001, 64, 7000, "f16", "none", 0.1, "twice"),
+    (16640, 64, 10001, "bf16", "none", 0.2, "any"),     # pieces of the vocabulary
+    (2100, 72, 130001, "bf16", "none", 0.0, "any"),     # big tiles
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,H,V,dtype,reduction,masked,targets", CASES)
+def test_gradients_are_as_far_off_as_foretold(rows, H, V, dtype, reduction, masked, targets):
+    """Written, and added to buffers that hold values of the gradient's own size."""
+    hidden, W, t, b, gl = make("cuda", rows, H, V, dtype, reduction, masked, targets)
+    c = Centred(hidden, W, t, bias=b, reduction=reduction, grad_loss=gl)
+    assert_as_foretold(c, gradients(hidden, W, t, b, gl, reduction))
+    g = torch.Generator(device="cuda").manual_seed(9)
+    base_W, base_b = ((torch.randn(x.shape, generator=g, device="cuda") * x.square().mean().sqrt())
+                      .to(hidden.dtype) for x in (c.d_W(c.d), c.d_bias(c.d)))
+    out = (None, base_W.clone(), base_b.clone())
+    gradients(hidden, W, t, b, gl, reduction, out=out, accumulate=True)
+    assert_as_foretold(c, out, base_W, base_b)
+
+
 # ------------------------------------------------------------------ d_bias
 
 def bias_bound(c, base=None):
@@ -68,13 +134,6 @@ def test_the_bound_of_d_bias_tells_sums_of_rounded_entries(rows, dtype):
     assert_close(rounded(c.d_bias(c.d), c.dtype), want, tol, "d_bias")
     with pytest.raises(AssertionError):
         assert_close(rounded(c.d_bias(c.round_d()), c.dtype), want, tol, "d_bias")
-
-
-def gradients(hidden, W, t, b, gl, reduction, **kw):
-    loss, lse = lm.cross_entropy_f32(hidden, W, t, bias=b, reduction=reduction)
-    got = lm.cross_entropy_grad(hidden, W, t, lse, gl, bias=b, reduction=reduction, **kw)
-    check_status()
-    return got
 
 
 @pytest.mark.gpu

@@ -90,3 +90,35 @@ class Centred:
 
 def rounded(x, dtype):
     return x.float().to(dtype).double()
+
+
+def error(got, want):
+    return float((got.double() - want).norm())
+
+
+def foretold(c, exact, as_used, own):
+    """The largest 2-norm of an output's error: `exact` it is, `as_used` it would be with d as the
+    products have it, `own` the size of the part that the logits' errors act on."""
+    e = error(rounded(as_used, c.dtype), exact)
+    return SLACK * (e ** 2 + (c.logits * float(own.norm())) ** 2) ** 0.5
+
+
+def assert_as_foretold(c, got, base_W=None, base_bias=None):
+    """got = (d_hidden, d_W, d_bias), any of them None: each as a whole, d_W also on the rows that are
+    some row's target and on the others."""
+    exact = c.outputs(c.d, base_W, base_bias)
+    used = c.round_d()
+    as_used = c.outputs(used, base_W, base_bias)[:2] + (exact[2],)
+    own = c.outputs(c.d)
+    hit = torch.zeros(c.w.shape[0], dtype=torch.bool, device=c.d.device)
+    hit[c.t] = True
+    for i, name in enumerate(("d_hidden", "d_W", "d_bias")):
+        if got[i] is None:
+            continue
+        parts = [("", slice(None))]
+        if i == 1:
+            parts += [(" of the targets", hit), (" of the other entries", ~hit)]
+        for what, at in parts:
+            off = error(got[i][at], exact[i][at])
+            most = foretold(c, exact[i][at], as_used[i][at], own[i][at])
+            assert off <= most, (name + what, off / most)
