@@ -1510,7 +1510,8 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  const int k = top > 0.0f ? min(100, max(-100, 13 - ilogbf(top))) : 0;
+  // (2^k and 2^-k stay normal numbers: top may be any fp32 value)
+  const int k = top > 0.0f ? min(126, 13 - ilogbf(top)) : 0;
   const float up = ldexpf(1.0f, k), down = ldexpf(1.0f, -k);
   for (int32_t i = (int32_t)blockIdx.x * kRowsBlock + warp; i < n;
        i += (int32_t)gridDim.x * kRowsBlock) {

@@ -10,7 +10,7 @@ import torch
 import fp32_accumulate_lm_b200 as lm
 from gpu_helpers import check_status
 from training_precision import IGNORE, Centred, assert_as_foretold, rounded
-from training_reference import assert_close, half_step
+from training_reference import CrossEntropy, assert_close, half_step
 
 DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
 
@@ -154,3 +154,28 @@ def test_d_bias_is_summed_in_fp32(rows, V, masked, dtype):
     added = base.clone()
     gradients(hidden, W, t, b, gl, "none", out=(None, None, added), accumulate=True)
     assert_close(added, *bias_bound(c, base), "d_bias, added")
+
+
+# ------------------------------------------------------------------ weights
+
+def step(hidden, W, t, gl, alpha=1.0):
+    loss, lse = lm.cross_entropy_f32(hidden, W, t, alpha=alpha, reduction="none")
+    grads = lm.cross_entropy_grad(hidden, W, t, lse, gl, alpha=alpha, reduction="none")
+    check_status()
+    return grads, CrossEntropy(hidden, W, t, alpha=alpha, reduction="none", grad_loss=gl)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("log2", [(120, -110), (126, -116), (-100, 90)])
+def test_weights_as_far_from_1_as_alpha(rows, dtype, log2):
+    """Upstream gradients near fp32's limits, which alpha brings back: fp16's range holds the entries
+    of d without either."""
+    hidden, W, t, _, gl = make("cuda", rows, 64, 500, dtype)
+    up, alpha = 2.0 ** log2[0], 2.0 ** log2[1]
+    if alpha > 1:  # all logits 0: what alpha would make of them fp32 could not hold
+        W.zero_()
+    grads, ref = step(hidden, W, t, gl.clamp(-1.9, 1.9) * up, alpha)
+    assert_close(grads[0], ref.d_hidden, ref.d_hidden_tol, "d_hidden")
+    assert_close(grads[1], ref.d_W, ref.d_W_tol, "d_W")
