@@ -179,3 +179,65 @@ def test_weights_as_far_from_1_as_alpha(rows, dtype, log2):
     grads, ref = step(hidden, W, t, gl.clamp(-1.9, 1.9) * up, alpha)
     assert_close(grads[0], ref.d_hidden, ref.d_hidden_tol, "d_hidden")
     assert_close(grads[1], ref.d_W, ref.d_W_tol, "d_W")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [60, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_weights_of_very_different_sizes(rows, dtype):
+    """Down to 2^-28 of the largest. The power of two is common to the call: an entry of fp16's d is
+    off by half a step, or by 2^-38 of the largest factor where that is more."""
+    hidden, W, t, _, gl = make("cuda", rows, 64, 3000, dtype)
+    gl = gl.sign() * 2.0 ** -(torch.arange(rows, device="cuda") % 29).float() * 4096
+    grads, ref = step(hidden, W, t, gl)
+    assert_close(grads[0], ref.d_hidden, ref.d_hidden_tol, "d_hidden")
+    assert_close(grads[1], ref.d_W, ref.d_W_tol, "d_W")
+
+
+# ------------------------------------------------------------------ rows sure of a wrong entry
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,V", [(96, 3000), (700, 3000), (2100, 130001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_sure_of_a_wrong_entry(rows, V, dtype):
+    """Their entry of d at the wrong entry is as large as the target's and is rounded to 16 bits
+    unmended: the errors are those foretold, past what rounding the gradients alone gives."""
+    hidden, W, t, b, gl = make("cuda", rows, 64, V, dtype, sure=math.log(V) + 1)
+    c = Centred(hidden, W, t, reduction="none", grad_loss=gl)
+    p = (c.d / gl.double()[c.rows][:, None])[c.at, (c.t + 1) % V]
+    assert 0.3 < float(p.mean()) < 0.95
+    loss, lse = lm.cross_entropy_f32(hidden, W, t, reduction="none")
+    got = lm.cross_entropy_grad(hidden, W, t, lse, gl, reduction="none")
+    check_status()
+    assert_as_foretold(c, got)
+
+
+# ------------------------------------------------------------------ the loss of rows sure of their target
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,V", [(1, 1024), (40, 1024), (300, 5000)])
+def test_small_losses_keep_their_bits(rows, V):
+    """Logits that fp32 holds exactly in any order of summation (multiples of 2^-8 below 2^8), so all
+    that is off comes behind them. Each term of the sum, 2^(x - x_t) with x = z log2(e), is off by the
+    rounding of log2(e), of x and of x_t, |x| 2^-24 each, in the exponent (times log 2), by 2^-22 in
+    exp2 and by its way through at most 60 sums and rescalings, 2^-22 each, and log1p by 2^-22."""
+    g = torch.Generator(device="cuda").manual_seed(rows + V)
+    H = 64
+    W = torch.randint(-4, 5, (V, H), generator=g, device="cuda").float() / 16
+    t = torch.randint(0, V, (rows,), generator=g, device="cuda")
+    hidden = torch.randint(-8, 9, (rows, H), generator=g, device="cuda").float() / 16
+    # units along the target's row, for a loss of 1e-1 to 1e-5
+    lead = torch.randint(2, 5, (rows, 1), generator=g, device="cuda").float()
+    hidden += W[t].sign() * lead
+    hidden, W, t = hidden.bfloat16(), W.bfloat16(), t.to(torch.int32)
+    z = hidden.double() @ W.double().t()
+    assert float(z.abs().max()) < 2 ** 8 and torch.equal(z * 2 ** 8, (z * 2 ** 8).round())
+    zt = z.gather(1, t.long()[:, None])
+    others = z.scatter(1, t.long()[:, None], float("-inf"))
+    want = torch.log1p(torch.exp(others - zt).sum(1))
+    loss, lse = lm.cross_entropy_f32(hidden, W, t, reduction="none")
+    check_status()
+    assert float(want.min()) < 1e-4 or rows == 1
+    x = z.abs().amax(1) * 1.4427
+    tol = want * ((4 * x) * 2.0 ** -24 * 0.6932 + 63 * 2.0 ** -22)
+    assert_close(loss, want, tol, "loss")
