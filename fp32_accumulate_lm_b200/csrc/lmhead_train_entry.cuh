@@ -96,7 +96,8 @@ struct XentPieces {
 
 // How many parts dH's K (a piece) is split into, at 512 entries a part or more; each has an fp32
 // buffer of its own, and they are added in order at the end. For dH alone its tiles are as many as
-// the device has units, and no more, as a second round costs a whole tile's time (96 x 2048 x
+// a B200 has units (148 SMs, 74 pairs: constants, since the workspace's size is asked for without a
+// device), and no more, as a second round costs a whole tile's time (96 x 2048 x
 // 151936: 259 us with 18 splits of 8 tiles on 148 SMs, 287 with 19). Beside dW they leave units to
 // dW's tiles, so that the one reads W while the other writes: 2/5 of the units for lone CTAs, where
 // memory bounds both (both gradients of 8 x 1024 x 50304: 108 us with 14 splits, 127 with 32; of 32

@@ -300,9 +300,11 @@ int lmhead_nvfp4_quantize_noalloc(const void* w, int64_t V, int64_t H, uint8_t* 
  * accumulate != 0 adds d_W and d_bias to what these buffers hold (in fp32, rounded once); d_hidden
  * is always written. Any of the three may be NULL and is then not computed, but not all of them. A
  * row with a target outside [0, V) that is not ignored has NaN gradients, and so have d_W and
- * d_bias then. The products take dz in the operands' 16-bit type (each entry off by at most half a
- * step of that type, fp16 with a common power of two taken out); every sum is fp32, and d_bias sums dz
- * as it is before that rounding.
+ * d_bias then. The products take dz in the operands' 16-bit type: each entry is off by at most half a
+ * step of that type, but for the target's, which enters in fp32. For fp16 a power of two is taken out
+ * of the whole call, so an entry is off by 2^-38 of the call's largest |g_r (1 + 2 z_loss lse)| instead
+ * where that is more (rows weighted far below the largest). Every sum is fp32, and d_bias sums dz as it
+ * is before that rounding.
  *
  * Both are deterministic. The loss and lse of a row do not depend on the other rows of the call, bit
  * for bit; the gradients' sums run over the rows that count in order, and d_hidden's over parts of the
