@@ -1396,7 +1396,7 @@ __global__ void __launch_bounds__(1024)
     s = __shfl_sync(0xffffffffu, s, 0);
     if (held) {
       const float xt = zt * kLog2e;
-      if (xt == INFINITY) {  // inf - inf, as for +inf elsewhere in the row
+      if (zt == INFINITY) {  // inf - inf, as for +inf elsewhere in the row
         loss = lse = __int_as_float(0x7fc00000);
       } else if (xt >= m) {
         loss = log1pf(s * exp2f(m - xt));

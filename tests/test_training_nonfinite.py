@@ -113,3 +113,15 @@ def test_a_target_at_minus_infinity(rows):
     tol = (p[3] @ W.double().abs()) * (2.0 ** -8 + 2.0 ** -12) + 2.0 ** -8 * want.abs() \
         + (W[40].double().abs()) * 2.0 ** -20
     assert ((grads[0][3].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("rows", [5, 140, 300])
+def test_a_target_near_the_largest_number(rows):
+    """A logit that is finite, though its product with log2(e) is not: sure of its target."""
+    hidden, W, targets, bias = make(rows, 64, 300)
+    bias[17] = 3e38
+    targets.fill_(17)
+    loss, lse, grads = step(hidden, W, targets, bias)
+    assert torch.count_nonzero(loss) == 0 and (lse == bias[17].float()).all()
+    for g in grads:
+        assert not g.any()
